@@ -480,6 +480,185 @@ asm_status asm_decode_step_search(const void *q, const void *q_search,
                                   cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Paged serving                                                            */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * A serving loop keeps its requests' local tokens in pages of S tokens and
+ * handles several requests, new tokens per request and shared prefixes at
+ * once.  These calls cover one step of it (the paper has no counterpart):
+ *   asm_page_step         page tables and slots of the step's new tokens
+ *   asm_rope_append       rotary positions of q, k; k, v into their pages
+ *   asm_shared_plan       the step's work list, shared by all layers
+ *   asm_shared_attention  attention over prefix and local pages
+ * Common terms: R rows (requests) of the batch, at most 4096; T, the token
+ * capacity of the batch (its arrays' length); the new tokens of row r are
+ * q_off[r] .. q_off[r+1]-1.  S (page_size) is 16, 32, 64 or 128.  A page cache
+ * is [n_pages, Hkv, S, d] dt, one for k and one for v; the token with index x
+ * of a row lies at place x % S of page table[r, x / S], its slot is
+ * table[r, x / S] * S + x % S.  Lengths and ids are read on the device, so
+ * every call can be captured into a graph and replayed with other lengths.
+ */
+
+/*
+ * asm_page_step -- page tables and slot maps of one step, from the rows'
+ * lengths.  Free pages form a ring: pool[(head + i) % F] for i < count.
+ *   kv_len     [R]   tokens the row holds before the step
+ *   new_len    [R]   new tokens; 0 for none; negative: the row ends, it holds
+ *                    nothing any more and its pages go back to the ring, behind
+ *                    the free ones, in row order
+ *   pos_base   [R]   added to the row's positions (its prefix length), or NULL
+ *   table      [R, max_pages] in/out: granted pages are added, every other
+ *                    entry stays (those of an ended row as well)
+ *   pool       [F]   in/out; F counts all pages, held and free
+ *   pool_state [3]   head, count, (unused)
+ *   seq_len    [R]   out: tokens the row holds after the step
+ *   q_off      [R+1] out: row offsets in the token batch, at most T
+ *   row, pos, slot [T] out, per token: its row, its position
+ *                    pos_base[r] + index, its slot.  Tokens behind the last
+ *                    row: -1, 0, -1
+ *   pool_out   [3]   out: head, count, refused rows
+ * All int32, on the device; page_size x F and page_size x max_pages must stay
+ * below 2^31 (ASM_ERR_INVALID_ARG).  A row is granted all its pages or none:
+ * it is refused if its tokens end past T, if its table is too short, or if
+ * the pages asked for by the rows up to it exceed the free ones; pages
+ * returned by this step serve the next one.  A refused row keeps its length
+ * and pages, its tokens get slot -1.  Lengths below 0 or above the table are
+ * clamped.  The step's inputs are not changed (the ring and the table only
+ * where nothing is read), so outputs may not be the inputs: feed seq_len and
+ * pool_out to the next call.  No workspace; one launch.
+ */
+asm_status asm_page_step(const int32_t *kv_len, const int32_t *new_len,
+                         const int32_t *pos_base, int R, int page_size,
+                         int max_pages, int32_t *table, int32_t *pool,
+                         const int32_t *pool_state, int F, int T,
+                         int32_t *seq_len, int32_t *q_off, int32_t *row,
+                         int32_t *pos, int32_t *slot, int32_t *pool_out,
+                         cudaStream_t stream);
+
+/* Which elements of a head form pair i of rot / 2: i and i + rot / 2 (HALF),
+ * or 2i and 2i + 1 (PAIRS, interleaved).  Elements from rot on do not turn. */
+typedef enum { ASM_ROPE_HALF = 0, ASM_ROPE_PAIRS = 1 } asm_rope_layout;
+
+/* Frequencies for long contexts, f_i = theta^(-2i / rot) scaled by `factor`:
+ *   LINEAR  f_i / factor
+ *   BASE    theta x factor^(rot / (rot - 2)) as the base
+ *   BANDS   w f_i + (1 - w) f_i / factor, w = (n_i - lo) / (hi - lo) in
+ *           [0, 1], n_i = ctx f_i / (2 pi) turns over the trained length ctx
+ *   YARN    the same blend with w falling linearly in the pair's index, from
+ *           the pair that makes hi turns over ctx to the one that makes lo
+ *           (pass the attention factor 0.1 ln(factor) + 1 as mscale) */
+typedef enum {
+    ASM_ROPE_SCALE_NONE = 0,
+    ASM_ROPE_SCALE_LINEAR = 1,
+    ASM_ROPE_SCALE_BASE = 2,
+    ASM_ROPE_SCALE_BANDS = 3,
+    ASM_ROPE_SCALE_YARN = 4
+} asm_rope_scaling;
+
+/*
+ * asm_rope_freqs -- freq[rot / 2] (fp64): the angle, in radians, that each
+ * pair turns per position.  rot even, 2 <= rot <= 128; theta > 1; factor >= 1;
+ * lo < hi and ctx >= 1 are read by BANDS and YARN only.  Callers may as well
+ * fill freq themselves.
+ */
+asm_status asm_rope_freqs(double *freq, int rot, double theta,
+                          asm_rope_scaling scaling, double factor, double lo,
+                          double hi, double ctx, cudaStream_t stream);
+
+/*
+ * asm_rope -- rotary positions of T tokens of H heads.  Pair (a, b) of a token
+ * at position p becomes
+ *   mscale (a cos pf - b sin pf, b cos pf + a sin pf);
+ * with inverse != 0 it turns back (the transpose of the call without it, so
+ * its gradient).  Angles are exact to 2^-32 turns at any int32 position.
+ *   x, y  token t, head h starts at element t * x_st + h * x_sh (y alike); d
+ *         contiguous elements.  y may be x (same strides: in place), else
+ *         they must not overlap; y's strides must be at least d
+ *   pos   [T] int32;  freq [rot / 2] fp64;  rot even, 2 <= rot <= d
+ * fp32 arithmetic (bf16 sines to 2^-21), rounded to dt once.  16-byte aligned
+ * heads and rot a multiple of 16 (bf16) or 8 (fp32) run vectorised; all others
+ * element by element.
+ */
+asm_status asm_rope(const void *x, int64_t x_st, int64_t x_sh, int T, int H,
+                    int d, asm_dtype dt, const int32_t *pos, const double *freq,
+                    int rot, asm_rope_layout layout, float mscale, int inverse,
+                    void *y, int64_t y_st, int64_t y_sh, cudaStream_t stream);
+
+/*
+ * asm_rope_append -- q_out = asm_rope(q); asm_rope(k) and v into the page
+ * caches at the tokens' slots.  Tokens whose slot lies outside
+ * [0, n_pages x page_size) store nothing (q is still turned).  Two tokens must
+ * not have the same slot.  q, k, v are strided as in asm_rope (views of one
+ * packed projection, for example); q_out may be q.  The caches must not
+ * overlap the other arrays.  One launch.
+ */
+asm_status asm_rope_append(const void *q, int64_t q_st, int64_t q_sh,
+                           const void *k, int64_t k_st, int64_t k_sh,
+                           const void *v, int64_t v_st, int64_t v_sh, int T,
+                           int Hq, int Hkv, int d, asm_dtype dt,
+                           const int32_t *pos, const int32_t *slot,
+                           const double *freq, int rot, asm_rope_layout layout,
+                           float mscale, void *q_out, int64_t o_st,
+                           int64_t o_sh, void *k_pages, void *v_pages,
+                           int n_pages, int page_size, cudaStream_t stream);
+
+/*
+ * asm_shared_plan -- the work list of asm_shared_attention for a step's
+ * lengths, made on the device; all layers of the step share it.
+ *   q_off      [R+1] token offsets of the rows (asm_page_step's)
+ *   seq_len    [R]   local tokens of the row, its new ones included
+ *   group_off  [NG+1] rows group_off[j] .. group_off[j+1]-1 share prefix j; rows
+ *                    before and behind have none.  NULL with NG = 0
+ *   prefix_len [NG]  tokens of each prefix
+ * Offsets that fall are raised to the largest before them, offsets and
+ * lengths beyond T, R, the tables' pages are clamped.
+ *   plan       asm_shared_plan_size(R, NG, T, Hq, Hkv) bytes (any content)
+ * NG <= 4096, T <= 2^24.  The plan belongs to these sizes and to the device it
+ * was made on.  One launch.
+ */
+size_t asm_shared_plan_size(int R, int NG, int T, int Hq, int Hkv);
+asm_status asm_shared_plan(const int32_t *q_off, const int32_t *seq_len,
+                           const int32_t *group_off, const int32_t *prefix_len,
+                           int R, int NG, int T, int Hq, int Hkv, int page_size,
+                           int max_pages, int max_prefix_pages, void *plan,
+                           size_t plan_bytes, cudaStream_t stream);
+
+/*
+ * asm_shared_attention -- attention of the batch's new tokens over the prefix
+ * of their row's group and over the row's own tokens up to themselves: the new
+ * token i of n of row r sees the whole prefix and the local keys
+ * 0 .. seq_len[r] - n + i.  A prefix is read once for all the rows that share
+ * it (per 256 query rows), in contrast to asm_flash_decode for any number of
+ * prefixes, new tokens per row and pages.
+ *   q, out       [T, Hq, d] dt
+ *   k_pages, v_pages [n_pages, Hkv, S, d] dt (the new tokens' included)
+ *   table        [R, max_pages] int32, prefix_table [NG, max_prefix_pages]
+ *   lse_out      [T, Hq] fp32 (natural log), or NULL
+ *   plan         of asm_shared_plan with the same sizes
+ *   scale        > 0 and finite
+ *   ws           asm_shared_attention_workspace_size(...) bytes, word 0 zeroed
+ *                once (asm_workspace_init); asm_workspace_error reads it
+ * A token without any key gets (0, -inf).  Tokens outside every row are left
+ * as they were.  Keys behind a row's length are not used, whatever their
+ * pages hold.  A page id outside [0, n_pages) reads as zeros and sets the error
+ * word to ASM_ERR_INVALID_ARG, and so does a plan of other sizes, with which
+ * the call writes nothing.  (out, lse_out) is an attention state: with
+ * asm_decode_step over no local tokens and asm_merge_states it joins the
+ * memory's retrieved state in place of an explicit prefix.
+ */
+size_t asm_shared_attention_workspace_size(int T, int Hq, int Hkv, int d);
+asm_status asm_shared_attention(const void *q, const void *k_pages,
+                                const void *v_pages, int n_pages, int page_size,
+                                const int32_t *table, int max_pages,
+                                const int32_t *prefix_table,
+                                int max_prefix_pages, const void *plan,
+                                size_t plan_bytes, int R, int NG, int T, int Hq,
+                                int Hkv, int d, float scale, asm_dtype dt,
+                                void *out, float *lse_out, void *ws,
+                                size_t ws_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Utilities                                                                */
 /* ------------------------------------------------------------------------ */
 

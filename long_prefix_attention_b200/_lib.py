@@ -14,6 +14,8 @@ LIB_PATH = os.path.join(_PKG, "libasm_b200.so")
 P = ctypes.c_void_p
 I = ctypes.c_int
 F = ctypes.c_float
+D = ctypes.c_double
+L = ctypes.c_int64
 SZ = ctypes.c_size_t
 
 # name -> (restype, argtypes); mirrors include/asm.h
@@ -45,6 +47,14 @@ SIGNATURES = {
     "asm_whiten": (I, [P, I, I, I, I, ctypes.c_int64, ctypes.c_int64, P, P, P, ctypes.c_int64, ctypes.c_int64, P]),
     "asm_decode_step_search": (I, [P, P, P, P, P, P, P, P, I, I, I, I, I, I, F, I, I, P, P, P, ctypes.c_uint, P,
                                    SZ, P]),
+    "asm_page_step": (I, [P, P, P, I, I, I, P, P, P, I, I, P, P, P, P, P, P, P]),
+    "asm_rope_freqs": (I, [P, I, D, I, D, D, D, D, P]),
+    "asm_rope": (I, [P, L, L, I, I, I, I, P, P, I, I, F, I, P, L, L, P]),
+    "asm_rope_append": (I, [P, L, L, P, L, L, P, L, L, I, I, I, I, I, P, P, P, I, I, F, P, L, L, P, P, I, I, P]),
+    "asm_shared_plan_size": (SZ, [I, I, I, I, I]),
+    "asm_shared_plan": (I, [P, P, P, P, I, I, I, I, I, I, I, I, P, SZ, P]),
+    "asm_shared_attention_workspace_size": (SZ, [I, I, I, I]),
+    "asm_shared_attention": (I, [P, P, P, I, I, P, I, P, I, P, SZ, I, I, I, I, I, I, F, I, P, P, P, SZ, P]),
     "asm_workspace_init": (I, [P, SZ, P]),
     "asm_workspace_error": (I, [P, SZ, ctypes.POINTER(ctypes.c_int), P]),
     "asm_wait_spin_limit": (ctypes.c_uint32, []),

@@ -18,6 +18,12 @@ bool group_ok(int Hq, int Hkv) {
     return G == 1 || G == 2 || G == 4 || G == 8;
 }
 
+// Do [a, a + na) and [b, b + nb) share a byte?
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return na > 0 && nb > 0 && x < y + nb && y < x + na;
+}
+
 // Multiprocessor count of the current device (cached per device ordinal).
 int num_sms() {
     static int cache[64] = {0};
@@ -357,6 +363,161 @@ asm_status asm_flash_decode(const void *q, const void *k_prefix, const void *v_p
     return cuda_status(asm_decode_launch(1, q, nullptr, nullptr, nullptr, k_prefix, v_prefix, Lp, k_cache,
                                          v_cache, local_len, B, Hq, Hkv, 1, Tmax, d, scale, 0, dt, out,
                                          lse_out, nullptr, 0u, ws, num_sms(), stream));
+}
+
+// ---------------------------------------------------------- paged serving --
+
+static bool page_ok(int S) { return S == 16 || S == 32 || S == 64 || S == 128; }
+// n pages of S tokens: slots and lengths stay within int32
+static bool pages_fit(int n, int S) { return n >= 1 && (int64_t)n * S <= INT32_MAX; }
+
+asm_status asm_page_step(const int32_t *kv_len, const int32_t *new_len, const int32_t *pos_base, int R, int page_size,
+                         int max_pages, int32_t *table, int32_t *pool, const int32_t *pool_state, int F, int T,
+                         int32_t *seq_len, int32_t *q_off, int32_t *row, int32_t *pos, int32_t *slot,
+                         int32_t *pool_out, cudaStream_t stream) {
+    if (R < 1 || T < 0) return ASM_ERR_INVALID_ARG;
+    if (!page_ok(page_size) || R > 4096) return ASM_ERR_UNSUPPORTED;
+    if (!pages_fit(max_pages, page_size) || !pages_fit(F, page_size)) return ASM_ERR_INVALID_ARG;
+    if (!aligned(kv_len, 4) || !aligned(new_len, 4) || !aligned(table, 4) || !aligned(pool, 4) ||
+        !aligned(pool_state, 4) || !aligned(seq_len, 4) || !aligned(q_off, 4) || !aligned(pool_out, 4))
+        return ASM_ERR_INVALID_ARG;
+    if (pos_base && !aligned(pos_base, 4)) return ASM_ERR_INVALID_ARG;
+    if (T > 0 && (!aligned(row, 4) || !aligned(pos, 4) || !aligned(slot, 4))) return ASM_ERR_INVALID_ARG;
+    // every block reads the inputs: none of them may be an output
+    const void *in[4] = {kv_len, new_len, pos_base, pool_state};
+    const size_t in_n[4] = {(size_t)R, (size_t)R, pos_base ? (size_t)R : 0, 3};
+    const void *out[6] = {seq_len, q_off, row, pos, slot, pool_out};
+    const size_t out_n[6] = {(size_t)R, (size_t)R + 1, (size_t)T, (size_t)T, (size_t)T, 3};
+    for (int i = 0; i < 4; ++i)
+        for (int o = 0; o < 6; ++o)
+            if (overlap(in[i], 4 * in_n[i], out[o], 4 * out_n[o])) return ASM_ERR_INVALID_ARG;
+    return cuda_status(asm_page_step_launch(kv_len, new_len, pos_base, R, page_size, max_pages, table, pool,
+                                            pool_state, F, T, seq_len, q_off, row, pos, slot, pool_out, num_sms(),
+                                            stream));
+}
+
+asm_status asm_rope_freqs(double *freq, int rot, double theta, asm_rope_scaling scaling, double factor, double lo,
+                          double hi, double ctx, cudaStream_t stream) {
+    if (rot < 2 || rot % 2 != 0 || rot > 128 || !(theta > 1.0) || !(theta < 1e30)) return ASM_ERR_INVALID_ARG;
+    if (scaling < ASM_ROPE_SCALE_NONE || scaling > ASM_ROPE_SCALE_YARN) return ASM_ERR_INVALID_ARG;
+    if (scaling != ASM_ROPE_SCALE_NONE && !(factor >= 1.0 && factor < 1e30)) return ASM_ERR_INVALID_ARG;
+    if (scaling == ASM_ROPE_SCALE_BANDS || scaling == ASM_ROPE_SCALE_YARN)
+        if (!(lo > 0.0 && lo < hi && hi < 1e30) || !(ctx >= 1.0 && ctx < 1e30)) return ASM_ERR_INVALID_ARG;
+    if (!aligned(freq, 8)) return ASM_ERR_INVALID_ARG;
+    return cuda_status(asm_rope_freqs_launch(freq, rot, theta, (int)scaling, factor, lo, hi, ctx, stream));
+}
+
+static asm_status rope_args(int T, int d, asm_dtype dt, const int32_t *pos, const double *freq, int rot, int layout,
+                            float mscale) {
+    if (!dt_ok(dt) || T < 0 || !(mscale - mscale == 0.f)) return ASM_ERR_INVALID_ARG;
+    if (layout != ASM_ROPE_HALF && layout != ASM_ROPE_PAIRS) return ASM_ERR_INVALID_ARG;
+    if (!d_ok(d)) return ASM_ERR_UNSUPPORTED;
+    if (rot < 2 || rot > d || rot % 2 != 0) return ASM_ERR_INVALID_ARG;
+    if (T > 0 && (!aligned(pos, 4) || !aligned(freq, 8))) return ASM_ERR_INVALID_ARG;
+    return ASM_OK;
+}
+// strides of an input (any broadcast) and of an output (no two elements the same)
+static bool in_view(const void *p, int64_t st, int64_t sh, size_t es) { return aligned(p, es) && st >= 0 && sh >= 0; }
+static bool out_view(const void *p, int64_t st, int64_t sh, int T, int H, int d, size_t es) {
+    if (!aligned(p, es) || st < 0 || sh < 0) return false;
+    if (T <= 1) return H <= 1 || sh >= d;
+    if (H <= 1) return st >= d;
+    // token by token with the heads within, or head by head with the tokens within
+    return (sh >= d && st >= (int64_t)(H - 1) * sh + d) || (st >= d && sh >= (int64_t)(T - 1) * st + d);
+}
+
+asm_status asm_rope(const void *x, int64_t x_st, int64_t x_sh, int T, int H, int d, asm_dtype dt, const int32_t *pos,
+                    const double *freq, int rot, asm_rope_layout layout, float mscale, int inverse, void *y,
+                    int64_t y_st, int64_t y_sh, cudaStream_t stream) {
+    if (H < 1) return ASM_ERR_INVALID_ARG;
+    const asm_status v = rope_args(T, d, dt, pos, freq, rot, (int)layout, mscale);
+    if (v != ASM_OK) return v;
+    if (T == 0) return ASM_OK;
+    const size_t es = dt == ASM_BF16 ? 2 : 4;
+    if (!in_view(x, x_st, x_sh, es) || !out_view(y, y_st, y_sh, T, H, d, es)) return ASM_ERR_INVALID_ARG;
+    if (x == y && ((T > 1 && x_st != y_st) || (H > 1 && x_sh != y_sh))) return ASM_ERR_INVALID_ARG;
+    return cuda_status(asm_rope_launch(x, x_st, x_sh, T, H, d, dt, pos, freq, rot, (int)layout, mscale,
+                                       inverse ? 1 : 0, y, y_st, y_sh, num_sms(), stream));
+}
+
+asm_status asm_rope_append(const void *q, int64_t q_st, int64_t q_sh, const void *k, int64_t k_st, int64_t k_sh,
+                           const void *v, int64_t v_st, int64_t v_sh, int T, int Hq, int Hkv, int d, asm_dtype dt,
+                           const int32_t *pos, const int32_t *slot, const double *freq, int rot,
+                           asm_rope_layout layout, float mscale, void *q_out, int64_t o_st, int64_t o_sh,
+                           void *k_pages, void *v_pages, int n_pages, int page_size, cudaStream_t stream) {
+    if (Hq < 1 || Hkv < 1) return ASM_ERR_INVALID_ARG;
+    const asm_status s = rope_args(T, d, dt, pos, freq, rot, (int)layout, mscale);
+    if (s != ASM_OK) return s;
+    if (!page_ok(page_size)) return ASM_ERR_UNSUPPORTED;
+    if (!pages_fit(n_pages, page_size)) return ASM_ERR_INVALID_ARG;
+    if (T == 0) return ASM_OK;
+    const size_t es = dt == ASM_BF16 ? 2 : 4;
+    if (!in_view(q, q_st, q_sh, es) || !in_view(k, k_st, k_sh, es) || !in_view(v, v_st, v_sh, es) ||
+        !out_view(q_out, o_st, o_sh, T, Hq, d, es) || !aligned(slot, 4) || !aligned(k_pages, 16) ||
+        !aligned(v_pages, 16))
+        return ASM_ERR_INVALID_ARG;
+    if (q == q_out && ((T > 1 && q_st != o_st) || (Hq > 1 && q_sh != o_sh))) return ASM_ERR_INVALID_ARG;
+    const size_t cache = (size_t)n_pages * page_size * Hkv * d * es;
+    if (overlap(k_pages, cache, v_pages, cache)) return ASM_ERR_INVALID_ARG;
+    return cuda_status(asm_rope_append_launch(q, q_st, q_sh, k, k_st, k_sh, v, v_st, v_sh, T, Hq, Hkv, d, dt, pos,
+                                              slot, freq, rot, (int)layout, mscale, q_out, o_st, o_sh, k_pages,
+                                              v_pages, n_pages, page_size, num_sms(), stream));
+}
+
+// sizes of a shared-attention plan
+static asm_status shared_sizes(int R, int NG, int T, int Hq, int Hkv) {
+    if (R < 1 || NG < 0 || T < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return ASM_ERR_INVALID_ARG;
+    if (R > 4096 || NG > 4096 || T > (1 << 24) || Hq > 4096 || !group_ok(Hq, Hkv)) return ASM_ERR_UNSUPPORTED;
+    return ASM_OK;
+}
+
+size_t asm_shared_plan_size(int R, int NG, int T, int Hq, int Hkv) {
+    if (shared_sizes(R, NG, T, Hq, Hkv) != ASM_OK) return 0;
+    return asm_shared_plan_bytes(R, NG, T, Hq, Hkv);
+}
+
+asm_status asm_shared_plan(const int32_t *q_off, const int32_t *seq_len, const int32_t *group_off,
+                           const int32_t *prefix_len, int R, int NG, int T, int Hq, int Hkv, int page_size,
+                           int max_pages, int max_prefix_pages, void *plan, size_t plan_bytes, cudaStream_t stream) {
+    const asm_status v = shared_sizes(R, NG, T, Hq, Hkv);
+    if (v != ASM_OK) return v;
+    if (!page_ok(page_size)) return ASM_ERR_UNSUPPORTED;
+    if (!pages_fit(max_pages, page_size) || (NG > 0 && !pages_fit(max_prefix_pages, page_size)))
+        return ASM_ERR_INVALID_ARG;
+    if (!aligned(q_off, 4) || !aligned(seq_len, 4)) return ASM_ERR_INVALID_ARG;
+    if (NG > 0 && (!aligned(group_off, 4) || !aligned(prefix_len, 4))) return ASM_ERR_INVALID_ARG;
+    if (!aligned(plan, 16) || plan_bytes < asm_shared_plan_bytes(R, NG, T, Hq, Hkv)) return ASM_ERR_WORKSPACE;
+    return cuda_status(asm_shared_plan_launch(q_off, seq_len, group_off, prefix_len, R, NG, T, Hq, Hkv, page_size,
+                                              max_pages, NG > 0 ? max_prefix_pages : 0, plan, num_sms(), stream));
+}
+
+size_t asm_shared_attention_workspace_size(int T, int Hq, int Hkv, int d) {
+    if (shared_sizes(1, 0, T, Hq, Hkv) != ASM_OK || !d_ok(d)) return 0;
+    return asm_shared_attention_ws_bytes(T, Hq, d, num_sms());
+}
+
+asm_status asm_shared_attention(const void *q, const void *k_pages, const void *v_pages, int n_pages, int page_size,
+                                const int32_t *table, int max_pages, const int32_t *prefix_table,
+                                int max_prefix_pages, const void *plan, size_t plan_bytes, int R, int NG, int T,
+                                int Hq, int Hkv, int d, float scale, asm_dtype dt, void *out, float *lse_out, void *ws,
+                                size_t ws_bytes, cudaStream_t stream) {
+    const asm_status v = shared_sizes(R, NG, T, Hq, Hkv);
+    if (v != ASM_OK) return v;
+    if (!dt_ok(dt) || !(scale > 0.f) || !(scale < 1e30f)) return ASM_ERR_INVALID_ARG;
+    if (!d_ok(d) || !page_ok(page_size)) return ASM_ERR_UNSUPPORTED;
+    if (!pages_fit(n_pages, page_size) || !pages_fit(max_pages, page_size) ||
+        (NG > 0 && !pages_fit(max_prefix_pages, page_size)) || (int64_t)n_pages * Hkv > INT32_MAX)
+        return ASM_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(table, 4) || !aligned(out, 16))
+        return ASM_ERR_INVALID_ARG;
+    if ((NG > 0 && !aligned(prefix_table, 4)) || (lse_out && !aligned(lse_out, 4))) return ASM_ERR_INVALID_ARG;
+    if (!aligned(plan, 16) || plan_bytes < asm_shared_plan_bytes(R, NG, T, Hq, Hkv)) return ASM_ERR_WORKSPACE;
+    if (!aligned(ws, 16) || ws_bytes < asm_shared_attention_ws_bytes(T, Hq, d, num_sms())) return ASM_ERR_WORKSPACE;
+    const size_t bytes = (size_t)T * Hq * d * (dt == ASM_BF16 ? 2 : 4);
+    if (overlap(q, bytes, out, bytes)) return ASM_ERR_INVALID_ARG;  // a tile's queries are read several times
+    return cuda_status(asm_shared_attention_launch(q, k_pages, v_pages, n_pages, page_size, table, max_pages,
+                                                   prefix_table, NG > 0 ? max_prefix_pages : 0, plan, R, NG, T, Hq,
+                                                   Hkv, d, scale, dt, out, lse_out, ws, num_sms(), stream));
 }
 
 asm_status asm_workspace_init(void *ws, size_t ws_bytes, cudaStream_t stream) {

@@ -113,3 +113,35 @@ cudaError_t asm_whitening_launch(const void *x, int H, int N, int d, asm_dtype d
 cudaError_t asm_whiten_launch(const void *x, int H, int R, int d, asm_dtype dt, long long sh_in, long long sr_in,
                               const float *mu, const float *W, void *y, long long sh_out, long long sr_out,
                               cudaStream_t st);
+
+// pages.cu: page tables and slot maps of one step
+cudaError_t asm_page_step_launch(const int32_t *kv_len, const int32_t *new_len, const int32_t *pos_base, int R,
+                                 int page_size, int max_pages, int32_t *table, int32_t *pool,
+                                 const int32_t *pool_state, int F, int T, int32_t *seq_len, int32_t *q_off,
+                                 int32_t *row, int32_t *pos, int32_t *slot, int32_t *pool_out, int num_sms,
+                                 cudaStream_t st);
+
+// rope.cu: rotary positions (strides in elements)
+cudaError_t asm_rope_freqs_launch(double *freq, int rot, double theta, int scaling, double factor, double lo,
+                                  double hi, double ctx, cudaStream_t st);
+cudaError_t asm_rope_launch(const void *x, int64_t x_st, int64_t x_sh, int T, int H, int d, asm_dtype dt,
+                            const int32_t *pos, const double *freq, int rot, int layout, float mscale, int inverse,
+                            void *y, int64_t y_st, int64_t y_sh, int num_sms, cudaStream_t st);
+cudaError_t asm_rope_append_launch(const void *q, int64_t q_st, int64_t q_sh, const void *k, int64_t k_st,
+                                   int64_t k_sh, const void *v, int64_t v_st, int64_t v_sh, int T, int Hq, int Hkv,
+                                   int d, asm_dtype dt, const int32_t *pos, const int32_t *slot, const double *freq,
+                                   int rot, int layout, float mscale, void *q_out, int64_t o_st, int64_t o_sh,
+                                   void *k_pages, void *v_pages, int n_pages, int page_size, int num_sms,
+                                   cudaStream_t st);
+
+// shared_plan.cu, shared_attn.cu: attention of a ragged batch over shared prefixes and paged local tokens
+size_t asm_shared_plan_bytes(int R, int NG, int T, int Hq, int Hkv);
+cudaError_t asm_shared_plan_launch(const int32_t *q_off, const int32_t *seq_len, const int32_t *group_off,
+                                   const int32_t *prefix_len, int R, int NG, int T, int Hq, int Hkv, int page_size,
+                                   int max_pages, int max_prefix_pages, void *plan, int num_sms, cudaStream_t st);
+size_t asm_shared_attention_ws_bytes(int T, int Hq, int d, int num_sms);
+cudaError_t asm_shared_attention_launch(const void *q, const void *k_pages, const void *v_pages, int n_pages,
+                                        int page_size, const int32_t *table, int max_pages,
+                                        const int32_t *prefix_table, int max_prefix_pages, const void *plan, int R,
+                                        int NG, int T, int Hq, int Hkv, int d, float scale, asm_dtype dt, void *out,
+                                        float *lse_out, void *ws, int num_sms, cudaStream_t st);

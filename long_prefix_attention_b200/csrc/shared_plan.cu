@@ -1,0 +1,240 @@
+// shared_plan.cu -- the plan of a shared-prefix attention call, made on the
+// GPU from the step's lengths.
+//
+// One block: running maxima make the offsets monotone whatever they hold,
+// then three sums over the rows, the groups and the tiles give the tile list,
+// the units before each tile and the partial rows before each tile.  Bound by
+// latency; a step's layers share one plan.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "launch.h"
+#include "shared.cuh"
+
+namespace asmk {
+namespace shared {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPer = kMaxRows / kPlanThreads;
+
+struct PlanArgs {
+    const int *q_off, *seq_len, *group_off, *prefix_len;
+    int R, NG, T, Hq, Hkv, S, max_pages, max_prefix_pages, workers;
+    char *plan;
+};
+
+template <typename Op>
+__device__ __forceinline__ long long plan_scan(long long v, long long *warp_v, long long zero, long long &tot, Op op) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, v, m);
+        if (lane >= m) v = op(o, v);
+    }
+    __syncthreads();
+    if (lane == 31) warp_v[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+        long long w = warp_v[lane];
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, w, m);
+            if (lane >= m) w = op(o, w);
+        }
+        warp_v[lane] = w;
+    }
+    __syncthreads();
+    tot = warp_v[31];
+    return warp > 0 ? op(warp_v[warp - 1], v) : op(zero, v);
+}
+
+// First index i < n with ends[i] > x (n if there is none); ends ascending.
+__device__ __forceinline__ int first_above(const int *ends, int n, int x) {
+    int lo = 0, hi = n;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (ends[mid] > x) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
+// off[0..n] = running maxima of src, kept within [0, hi].
+__device__ void monotone(const int *src, int *off, int n, int hi, long long *warp_v) {
+    const int per = (n + 1 + kPlanThreads - 1) / kPlanThreads, i0 = threadIdx.x * per;
+    long long m = 0, tot;
+    for (int i = i0; i < i0 + per && i <= n; ++i) m = max(m, (long long)min(max(src[i], 0), hi));
+    const long long inc = plan_scan(m, warp_v, 0, tot, [](long long a, long long b) { return max(a, b); });
+    // the maximum before this thread's entries: the inclusive one of its left neighbour
+    __shared__ int left[kPlanThreads];
+    left[threadIdx.x] = (int)inc;
+    __syncthreads();
+    int run = threadIdx.x > 0 ? left[threadIdx.x - 1] : 0;
+    for (int i = i0; i < i0 + per && i <= n; ++i) {
+        run = max(run, min(max(src[i], 0), hi));
+        off[i] = run;
+    }
+    __syncthreads();
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+shared_plan_kernel(const PlanArgs a) {
+    extern __shared__ int sm[];
+    __shared__ long long warp_v[32];
+    const int R = a.R, NG = a.NG, tid = threadIdx.x, G = a.Hq / a.Hkv;
+    int *qo = sm, *row_end = qo + R + 1, *go = row_end + R, *group_end = go + NG + 1;
+    const PlanLayout lay = plan_layout(R, NG, a.T, G);
+    Header *hdr = reinterpret_cast<Header *>(a.plan);
+    int *first = reinterpret_cast<int *>(a.plan + lay.first);
+    Tile *tiles = reinterpret_cast<Tile *>(a.plan + lay.tiles);
+    int2 *tok = reinterpret_cast<int2 *>(a.plan + lay.tok);
+    const auto add = [](long long x, long long y) { return x + y; };
+    const int dual = kDualRows / G;  // tokens of a 256-row tile
+    const int single = kTileRows / G;
+
+    monotone(a.q_off, qo, R, a.T, warp_v);
+    if (NG > 0) monotone(a.group_off, go, NG, R, warp_v);
+    // tiles of n tokens: one of up to 128 rows, else 256-row ones
+    auto n_tiles = [&](int n) { return n <= 0 ? 0 : n <= single ? 1 : (n + dual - 1) / dual; };
+    // groups first: theirs are the long key lists
+    long long tot, n_prefix = 0;
+    if (NG > 0) {
+        const int per = (NG + kPlanThreads - 1) / kPlanThreads, i0 = tid * per;
+        long long s = 0;
+        for (int i = i0; i < i0 + per && i < NG; ++i) s += n_tiles(qo[go[i + 1]] - qo[go[i]]);
+        long long e = plan_scan(s, warp_v, 0, n_prefix, add) - s;
+        for (int i = i0; i < i0 + per && i < NG; ++i) {
+            e += n_tiles(qo[go[i + 1]] - qo[go[i]]);
+            group_end[i] = (int)e;
+        }
+    }
+    {
+        const int per = (R + kPlanThreads - 1) / kPlanThreads, i0 = tid * per;
+        long long s = 0;
+        for (int i = i0; i < i0 + per && i < R; ++i) s += n_tiles(qo[i + 1] - qo[i]);
+        long long e = n_prefix + plan_scan(s, warp_v, 0, tot, add) - s;
+        for (int i = i0; i < i0 + per && i < R; ++i) {
+            e += n_tiles(qo[i + 1] - qo[i]);
+            row_end[i] = (int)e;
+        }
+    }
+    __syncthreads();
+    const int ntiles = (int)(n_prefix + tot);
+    // group of a row (-1: none) and its prefix length
+    auto prefix_of = [&](int r) {
+        if (NG == 0 || r < go[0] || r >= go[NG]) return -1;
+        return first_above(go + 1, NG, r);
+    };
+    auto prefix_keys = [&](int g) {
+        return (int)min((long long)max(a.prefix_len[g], 0), (long long)a.max_prefix_pages * a.S);
+    };
+    // ---- the tiles, and the units before each (chunks of one tile a thread)
+    long long before = 0;
+    for (int c = 0; c < ntiles; c += kPlanThreads) {
+        const int i = c + tid;
+        Tile t{};
+        if (i < ntiles) {
+            if (i < n_prefix) {
+                const int g = first_above(group_end, NG, i);
+                const int t0 = qo[go[g]], n = qo[go[g + 1]] - t0, per = n <= single ? n : dual;
+                const int j = i - (g > 0 ? group_end[g - 1] : 0);
+                t.tok0 = t0 + j * per;
+                t.ntok = min(per, n - j * per);
+                t.owner = g;
+                t.keys = prefix_keys(g);
+            } else {
+                const int r = first_above(row_end, R, i);
+                const int t0 = qo[r], n = qo[r + 1] - t0, per = n <= single ? n : dual;
+                const int j = i - (r > 0 ? row_end[r - 1] : (int)n_prefix);
+                const int len = (int)min((long long)max(a.seq_len[r], 0), (long long)a.max_pages * a.S);
+                t.tok0 = t0 + j * per;
+                t.ntok = min(per, n - j * per);
+                t.owner = r;
+                t.base = len - n + j * per;
+                t.keys = min(max(t.base + t.ntok, 0), len);
+                const int g = prefix_of(r);
+                t.flags = kLocal | ((g < 0 || prefix_keys(g) == 0) ? kDirect : 0);
+            }
+            t.units = (t.keys + kUnitKeys - 1) / kUnitKeys;
+        }
+        const long long inc = plan_scan(t.units, warp_v, 0, tot, add);
+        t.unit0 = before + inc - t.units;
+        before += tot;
+        if (i < ntiles) tiles[i] = t;
+    }
+    const long long W = before * a.Hkv;
+    long long upc = (W + a.workers - 1) / a.workers;
+    upc = upc < 1 ? 1 : upc;
+    if (upc > INT32_MAX) upc = INT32_MAX;  // a table cannot be that long
+    // ---- partial rows before each tile
+    before = 0;
+    for (int c = 0; c < ntiles; c += kPlanThreads) {
+        const int i = c + tid;
+        long long rows = 0;
+        int cap = 0;
+        if (i < ntiles && tiles[i].units > 0) {
+            cap = (int)(tiles[i].units / upc) + 2;
+            rows = (long long)cap * a.Hkv * tiles[i].ntok * G;
+        }
+        const long long inc = plan_scan(rows, warp_v, 0, tot, add);
+        if (i < ntiles) {
+            tiles[i].cap = cap;
+            tiles[i].row0 = before + inc - rows;
+            // the workers whose ranges begin in this tile
+            const long long u0 = tiles[i].unit0 * a.Hkv, u1 = u0 + (long long)tiles[i].units * a.Hkv;
+            for (long long w = (u0 + upc - 1) / upc; w * upc < u1; ++w) first[w] = i;
+        }
+        before += tot;
+    }
+    // ---- the tiles of every token
+    for (int t = tid; t < a.T; t += kPlanThreads) {
+        int2 v = make_int2(-1, -1);
+        if (t >= qo[0] && t < qo[R]) {
+            const int r = first_above(qo + 1, R, t);
+            const int n = qo[r + 1] - qo[r];
+            v.x = (r > 0 ? row_end[r - 1] : (int)n_prefix) + (n <= single ? 0 : (t - qo[r]) / dual);
+            const int g = prefix_of(r);
+            if (g >= 0) {
+                const int gn = qo[go[g + 1]] - qo[go[g]];
+                v.y = (g > 0 ? group_end[g - 1] : 0) + (gn <= single ? 0 : (t - qo[go[g]]) / dual);
+            }
+        }
+        tok[t] = v;
+    }
+    if (tid == 0) {
+        Header h{};
+        h.magic = kMagic;
+        h.R = R; h.NG = NG; h.T = a.T; h.Hq = a.Hq; h.Hkv = a.Hkv;
+        h.page_size = a.S; h.max_pages = a.max_pages; h.max_prefix_pages = a.max_prefix_pages;
+        h.workers = a.workers; h.ntiles = ntiles; h.upc = (int)upc; h.W = W;
+        *hdr = h;
+    }
+}
+
+}  // namespace shared
+}  // namespace asmk
+
+size_t asm_shared_plan_bytes(int R, int NG, int T, int Hq, int Hkv) {
+    return asmk::shared::plan_layout(R, NG, T, Hq / Hkv).total;
+}
+
+cudaError_t asm_shared_plan_launch(const int32_t *q_off, const int32_t *seq_len, const int32_t *group_off,
+                                   const int32_t *prefix_len, int R, int NG, int T, int Hq, int Hkv, int page_size,
+                                   int max_pages, int max_prefix_pages, void *plan, int num_sms, cudaStream_t st) {
+    using namespace asmk::shared;
+    PlanArgs a{};
+    a.q_off = q_off; a.seq_len = seq_len; a.group_off = group_off; a.prefix_len = prefix_len;
+    a.R = R; a.NG = NG; a.T = T; a.Hq = Hq; a.Hkv = Hkv;
+    a.S = page_size; a.max_pages = max_pages; a.max_prefix_pages = max_prefix_pages;
+    a.workers = num_sms < kMaxWorkers ? num_sms : kMaxWorkers;
+    a.plan = static_cast<char *>(plan);
+    const size_t smem = sizeof(int) * (2 * (size_t)R + 1 + 2 * (size_t)NG + 1);
+    if (smem > 40 * 1024) {  // beside the static arrays
+        cudaError_t e = cudaFuncSetAttribute(shared_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (4 * kMaxRows + 2) * (int)sizeof(int));
+        if (e != cudaSuccess) return e;
+    }
+    shared_plan_kernel<<<1, kPlanThreads, smem, st>>>(a);
+    return cudaGetLastError();
+}

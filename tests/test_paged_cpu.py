@@ -1,0 +1,191 @@
+"""Paged serving calls without a GPU: arguments are refused with the
+documented status before any CUDA call, and the plan's and the workspace's
+sizes cover what the kernels address."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+from long_prefix_attention_b200 import _lib, build, ops
+
+import paged_common as C
+
+INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
+NULL = None
+
+
+def at(i, off=0):
+    """Distinct fake addresses, 1 GiB apart, never dereferenced."""
+    return ctypes.c_void_p((i + 1) * (1 << 30) + off)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return _lib.load()
+
+
+def page_step(lib, **kw):
+    a = dict(kv=at(0), new=at(1), base=at(2), R=4, S=16, MP=8, table=at(3), pool=at(4), state=at(5), F=64, T=10,
+             seq=at(6), qoff=at(7), row=at(8), pos=at(9), slot=at(10), pout=at(11))
+    a.update(kw)
+    return lib.asm_page_step(a["kv"], a["new"], a["base"], a["R"], a["S"], a["MP"], a["table"], a["pool"], a["state"],
+                             a["F"], a["T"], a["seq"], a["qoff"], a["row"], a["pos"], a["slot"], a["pout"], None)
+
+
+def test_page_step_refusals(lib):
+    for kw in (dict(kv=NULL), dict(new=NULL), dict(table=NULL), dict(pool=NULL), dict(state=NULL), dict(seq=NULL),
+               dict(qoff=NULL), dict(pout=NULL), dict(row=NULL), dict(slot=at(10, 2)), dict(base=at(2, 1)),
+               dict(R=0), dict(T=-1), dict(F=0), dict(MP=0), dict(F=1 << 27), dict(MP=1 << 27),
+               dict(seq=at(0)), dict(pout=at(5)), dict(seq=at(1, 12)), dict(slot=at(2))):
+        assert page_step(lib, **kw) == INVALID, kw
+    assert page_step(lib, S=24) == UNSUPPORTED
+    assert page_step(lib, S=256) == UNSUPPORTED
+    assert page_step(lib, R=4097) == UNSUPPORTED
+
+
+def rope(lib, **kw):
+    a = dict(x=at(0), xt=512, xh=128, T=5, H=4, d=128, dt=1, pos=at(1), f=at(2), rot=128, lay=0, ms=1.0, inv=0, y=at(3),
+             yt=512, yh=128)
+    a.update(kw)
+    return lib.asm_rope(a["x"], a["xt"], a["xh"], a["T"], a["H"], a["d"], a["dt"], a["pos"], a["f"], a["rot"], a["lay"],
+                        a["ms"], a["inv"], a["y"], a["yt"], a["yh"], None)
+
+
+def test_rope_refusals(lib):
+    for kw in (dict(x=NULL), dict(y=NULL), dict(pos=NULL), dict(f=NULL), dict(f=at(2, 4)), dict(rot=0), dict(rot=130),
+               dict(rot=7), dict(lay=2), dict(dt=2), dict(H=0), dict(T=-1), dict(ms=math.nan), dict(ms=math.inf),
+               dict(xt=-1), dict(yt=128), dict(yh=0), dict(yh=64, yt=512), dict(x=at(0, 1)),
+               dict(y=at(0), yt=1024), dict(y=at(0), yh=256, yt=1024)):
+        assert rope(lib, **kw) == INVALID, kw
+    assert rope(lib, d=96) == UNSUPPORTED
+    assert rope(lib, T=0) == 0
+
+
+def test_rope_freqs_refusals(lib):
+    f = lib.asm_rope_freqs
+    assert f(NULL, 64, 1e4, 0, 1.0, 1.0, 4.0, 8192.0, None) == INVALID
+    assert f(at(0), 63, 1e4, 0, 1.0, 1.0, 4.0, 8192.0, None) == INVALID
+    assert f(at(0), 130, 1e4, 0, 1.0, 1.0, 4.0, 8192.0, None) == INVALID
+    assert f(at(0), 64, 1.0, 0, 1.0, 1.0, 4.0, 8192.0, None) == INVALID
+    assert f(at(0), 64, 1e4, 5, 1.0, 1.0, 4.0, 8192.0, None) == INVALID
+    assert f(at(0), 64, 1e4, 1, 0.5, 1.0, 4.0, 8192.0, None) == INVALID
+    assert f(at(0), 64, 1e4, 3, 2.0, 4.0, 4.0, 8192.0, None) == INVALID
+    assert f(at(0), 64, 1e4, 4, 2.0, 1.0, 4.0, 0.0, None) == INVALID
+
+
+def append(lib, **kw):
+    a = dict(q=at(0), k=at(1), v=at(2), T=5, Hq=8, Hkv=2, d=128, dt=1, pos=at(3), slot=at(4), f=at(5), rot=128, lay=0,
+             ms=1.0, qo=at(6), ot=1024, kp=at(7), vp=at(8), n=4, S=16)
+    a.update(kw)
+    return lib.asm_rope_append(a["q"], 1024, 128, a["k"], 256, 128, a["v"], 256, 128, a["T"], a["Hq"], a["Hkv"],
+                               a["d"], a["dt"], a["pos"], a["slot"], a["f"], a["rot"], a["lay"], a["ms"], a["qo"],
+                               a["ot"], 128, a["kp"], a["vp"], a["n"], a["S"], None)
+
+
+def test_rope_append_refusals(lib):
+    for kw in (dict(k=NULL), dict(v=NULL), dict(slot=NULL), dict(kp=NULL), dict(vp=at(8, 8)), dict(n=0), dict(n=1 << 27),
+               dict(Hkv=0), dict(Hq=0), dict(rot=126 + 4), dict(vp=at(7)), dict(vp=at(7, 1024)), dict(ot=512),
+               dict(qo=at(0), ot=2048)):
+        assert append(lib, **kw) == INVALID, kw
+    assert append(lib, S=8) == UNSUPPORTED
+    assert append(lib, d=80) == UNSUPPORTED
+    assert append(lib, T=0) == 0
+
+
+def plan(lib, **kw):
+    a = dict(qo=at(0), sl=at(1), go=at(2), pl=at(3), R=4, NG=2, T=100, Hq=8, Hkv=2, S=16, MP=8, MPP=8, plan=at(4),
+             nb=1 << 24)
+    a.update(kw)
+    return lib.asm_shared_plan(a["qo"], a["sl"], a["go"], a["pl"], a["R"], a["NG"], a["T"], a["Hq"], a["Hkv"], a["S"],
+                               a["MP"], a["MPP"], a["plan"], a["nb"], None)
+
+
+def attn(lib, **kw):
+    a = dict(q=at(0), k=at(1), v=at(2), n=64, S=16, t=at(3), MP=8, pt=at(4), MPP=8, plan=at(5), pb=1 << 24, R=4, NG=2,
+             T=100, Hq=8, Hkv=2, d=128, scale=0.1, dt=1, out=at(6), lse=at(7), ws=at(8), wb=1 << 29)
+    a.update(kw)
+    return lib.asm_shared_attention(a["q"], a["k"], a["v"], a["n"], a["S"], a["t"], a["MP"], a["pt"], a["MPP"],
+                                    a["plan"], a["pb"], a["R"], a["NG"], a["T"], a["Hq"], a["Hkv"], a["d"], a["scale"],
+                                    a["dt"], a["out"], a["lse"], a["ws"], a["wb"], None)
+
+
+def test_shared_attention_refusals(lib):
+    need = lib.asm_shared_plan_size(4, 2, 100, 8, 2)
+    assert need > 0
+    for kw in (dict(qo=NULL), dict(sl=NULL), dict(go=NULL), dict(pl=NULL), dict(R=0), dict(NG=-1), dict(T=0),
+               dict(Hkv=3), dict(MP=0), dict(MPP=0), dict(MP=1 << 28)):
+        assert plan(lib, **kw) == INVALID, kw
+    for kw in (dict(R=4097), dict(NG=4097), dict(T=(1 << 24) + 1), dict(Hq=32), dict(S=20)):
+        assert plan(lib, **kw) == UNSUPPORTED, kw
+    assert plan(lib, nb=need - 1) == WORKSPACE and plan(lib, plan=NULL) == WORKSPACE
+    wneed = lib.asm_shared_attention_workspace_size(100, 8, 2, 128)
+    for kw in (dict(q=NULL), dict(k=at(1, 8)), dict(v=NULL), dict(t=NULL), dict(pt=NULL), dict(out=NULL),
+               dict(lse=at(7, 2)), dict(n=0), dict(n=1 << 28), dict(dt=2), dict(scale=0.0), dict(scale=-1.0),
+               dict(scale=math.nan), dict(scale=math.inf), dict(out=at(0)), dict(out=at(0, 2048)), dict(T=0)):
+        assert attn(lib, **kw) == INVALID, kw
+    for kw in (dict(d=96), dict(S=512), dict(Hq=32), dict(R=5000)):
+        assert attn(lib, **kw) == UNSUPPORTED, kw
+    for kw in (dict(pb=need - 1), dict(plan=NULL), dict(ws=NULL), dict(wb=wneed - 1)):
+        assert attn(lib, **kw) == WORKSPACE, kw
+    assert lib.asm_shared_plan_size(4, 2, 100, 9, 2) == 0
+    assert lib.asm_shared_attention_workspace_size(100, 8, 2, 96) == 0
+
+
+def test_binding_refuses_host_tensors_and_other_types():
+    i = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        ops.asm_page_step(i, i, i, i, 16, i.view(1, 4), i, i, i, i, i, i)
+    x = torch.zeros(4, 2, 64)
+    with pytest.raises(ValueError):
+        ops.asm_rope(x, i, torch.zeros(32, dtype=torch.float64), x)
+    with pytest.raises(ValueError):
+        ops.asm_shared_attention(x, x, x, i, i, 1.0, x, i)
+    with pytest.raises(TypeError):
+        ops._i32("f", i.long())
+
+
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+def test_partial_rows_and_tiles_stay_within_their_bounds(lib, G):
+    """The plan's tile count and the partial rows it hands out, computed here
+    for random lengths, never exceed what the size functions provide for."""
+    import random
+    rng = random.Random(G)
+    Hkv, workers = 4, 148
+    Hq = G * Hkv
+    single, dual = 128 // G, 256 // G
+
+    def tiles(n):
+        return [] if n <= 0 else [n] if n <= single else [min(dual, n - i) for i in range(0, n, dual)]
+
+    for _ in range(200):
+        R, NG = rng.randint(1, 60), rng.randint(0, 4)
+        new = [rng.choice([0, 1, 1, 3, rng.randint(0, 900)]) for _ in range(R)]
+        T = max(1, sum(new))
+        cuts = sorted(rng.randint(0, R) for _ in range(NG + 1))
+        off = [0]
+        for n in new:
+            off.append(off[-1] + n)
+        lst = []
+        for g in range(NG):
+            pre = rng.choice([0, 1, 300, 40000])
+            lst += [(n, C.cdiv(pre, 128)) for n in tiles(off[cuts[g + 1]] - off[cuts[g]])]
+        for r in range(R):
+            old, done = rng.choice([0, 100, 9000]), 0
+            for n in tiles(new[r]):
+                done += n
+                lst.append((n, C.cdiv(old + done, 128)))
+        bound = min(R, T) + min(NG, T) + 2 * C.cdiv(T * G, 256)
+        assert len(lst) <= bound
+        W = Hkv * sum(u for _, u in lst)
+        upc = max(1, C.cdiv(W, workers))
+        rows = sum((u // upc + 2) * Hkv * n * G for n, u in lst if u)
+        assert rows <= 4 * T * Hq + (workers + 1) * 256
+        # segments of a pair never exceed its capacity
+        c0 = 0
+        for n, u in lst:
+            for _ in range(Hkv):
+                if u:
+                    assert (c0 + u - 1) // upc - c0 // upc + 1 <= u // upc + 2
+                c0 += u
