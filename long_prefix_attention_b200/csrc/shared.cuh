@@ -22,7 +22,7 @@ constexpr int kTileRows = 128, kDualRows = 256;
 constexpr int kMaxRows = 4096;   // batch rows (requests), and prefix groups
 constexpr int kMagic = 0x53504c4e;
 
-struct Tile {
+struct __align__(16) Tile {
     int tok0, ntok;    // tokens of the batch
     int owner;         // row (local) or group (prefix)
     int flags;         // kLocal / kDirect
@@ -112,6 +112,9 @@ __device__ __forceinline__ int segments(long long c0, int n, int upc) {
 __device__ __forceinline__ long long partial_row(const Tile &t, int G, int g, int s) {
     return t.row0 + ((long long)g * t.cap + s) * ((long long)t.ntok * G);
 }
+
+// shared_attn_tc.cu: the tensor-core kernel (bf16)
+cudaError_t launch_attn_tc(const AttnArgs &a, int num_sms, cudaStream_t st);
 
 }  // namespace shared
 }  // namespace asmk

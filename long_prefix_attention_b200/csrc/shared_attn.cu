@@ -47,7 +47,7 @@ struct Seg {
     long long prow;       // first partial row
 };
 
-template <typename T, int D>
+template <int D>
 __device__ void load_keys(const AttnArgs &a, const Seg &s, int kb, const int *list, Smem<D> &sm) {
     constexpr int LD = Smem<D>::LD, C = D / 4;
     const int tid = threadIdx.x;
@@ -69,8 +69,8 @@ __device__ void load_keys(const AttnArgs &a, const Seg &s, int kb, const int *li
         float kx[4] = {0.f, 0.f, 0.f, 0.f}, vx[4] = {0.f, 0.f, 0.f, 0.f};
         if (id >= 0) {
             const long long off = ((((long long)id * a.Hkv + s.g) << a.shift) + ((kb + r) & (a.S - 1))) * D + c;
-            load_vec<T, 4>(static_cast<const T *>(a.k_pages) + off, kx);
-            load_vec<T, 4>(static_cast<const T *>(a.v_pages) + off, vx);
+            load_vec<float, 4>(static_cast<const float *>(a.k_pages) + off, kx);
+            load_vec<float, 4>(static_cast<const float *>(a.v_pages) + off, vx);
         }
         store_vec<float, 4>(sm.k + r * LD + c, kx);
         store_vec<float, 4>(sm.v + r * LD + c, vx);
@@ -78,7 +78,7 @@ __device__ void load_keys(const AttnArgs &a, const Seg &s, int kb, const int *li
     __syncthreads();
 }
 
-template <typename T, int D, int MR>
+template <int D, int MR>
 __device__ void run_segment(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
     constexpr int LD = Smem<D>::LD, LP = Smem<D>::LP, BR = 16 * MR, NC = D / 64;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
@@ -92,8 +92,8 @@ __device__ void run_segment(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
             const int r = i / (D / 4), c = (i - r * (D / 4)) * 4, rr = rb + r;
             float x[4] = {0.f, 0.f, 0.f, 0.f};
             if (rr < rows)
-                load_vec<T, 4>(static_cast<const T *>(a.q) +
-                                   ((size_t)(s.t.tok0 + rr / a.G) * a.Hq + s.g * a.G + rr % a.G) * D + c, x);
+                load_vec<float, 4>(static_cast<const float *>(a.q) +
+                                       ((size_t)(s.t.tok0 + rr / a.G) * a.Hq + s.g * a.G + rr % a.G) * D + c, x);
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] *= a.sl2;
             store_vec<float, 4>(sm.q + r * LD + c, x);
@@ -111,7 +111,7 @@ __device__ void run_segment(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
         }
         for (int kb = s.k0; kb < s.k1; kb += kKB) {
             __syncthreads();
-            load_keys<T, D>(a, s, kb, list, sm);
+            load_keys<D>(a, s, kb, list, sm);
             float sc[MR][4];
 #pragma unroll
             for (int i = 0; i < MR; ++i)
@@ -201,7 +201,7 @@ __device__ void run_segment(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
                     float x[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[e] = o[i][4 * c + e] * inv;
-                    store_vec<T, 4>(static_cast<T *>(a.out) + th * D + 64 * c + 4 * tx, x);
+                    store_vec<float, 4>(static_cast<float *>(a.out) + th * D + 64 * c + 4 * tx, x);
                 }
                 if (a.lse && tx == 0) a.lse[th] = l[i] == 0.f ? kNegInf : (m[i] + log2f(l[i])) * kLn2;
             } else {
@@ -216,7 +216,7 @@ __device__ void run_segment(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
     }
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 shared_attn_kernel(const AttnArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -247,8 +247,8 @@ shared_attn_kernel(const AttnArgs a) {
             s.k1 = min((k + n) * kUnitKeys, s.t.keys);
             s.direct = (s.t.flags & kDirect) && n == s.t.units;
             s.prow = partial_row(s.t, a.G, s.g, w - (int)(c0 / h.upc));
-            if (s.t.ntok * a.G <= 16) run_segment<T, D, 1>(a, s, sm);
-            else run_segment<T, D, 4>(a, s, sm);
+            if (s.t.ntok * a.G <= 16) run_segment<D, 1>(a, s, sm);
+            else run_segment<D, 4>(a, s, sm);
             u += n;
             if (k + n == s.t.units && s.g == a.Hkv - 1) ++i;
         }
@@ -375,16 +375,23 @@ cudaError_t launch_merge(const AttnArgs &a, int num_sms, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <typename T, int D>
-cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t st) {
+template <int D>
+cudaError_t launch_f32(const AttnArgs &a, int num_sms, cudaStream_t st) {
     const size_t smem = sizeof(Smem<D>);
-    auto kern = shared_attn_kernel<T, D>;
+    auto kern = shared_attn_kernel<D>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<num_sms, kThreads, smem, st>>>(a);
+    kern<<<a.workers, kThreads, smem, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_merge<T, D>(a, num_sms, st);
+    return launch_merge<float, D>(a, num_sms, st);
+}
+
+template <int D>
+cudaError_t launch_bf16(const AttnArgs &a, int num_sms, cudaStream_t st) {
+    cudaError_t e = launch_attn_tc(a, num_sms, st);
+    if (e != cudaSuccess) return e;
+    return launch_merge<__nv_bfloat16, D>(a, num_sms, st);
 }
 
 }  // namespace shared
@@ -424,7 +431,6 @@ cudaError_t asm_shared_attention_launch(const void *q, const void *k_pages, cons
     a.ws_ml = reinterpret_cast<float2 *>(w + wl.ml);
     a.ws_o = reinterpret_cast<float *>(w + wl.o);
     a.ws_err = reinterpret_cast<int *>(w);
-    if (dt == ASM_BF16)
-        return d == 128 ? launch<__nv_bfloat16, 128>(a, num_sms, st) : launch<__nv_bfloat16, 64>(a, num_sms, st);
-    return d == 128 ? launch<float, 128>(a, num_sms, st) : launch<float, 64>(a, num_sms, st);
+    if (dt == ASM_BF16) return d == 128 ? launch_bf16<128>(a, num_sms, st) : launch_bf16<64>(a, num_sms, st);
+    return d == 128 ? launch_f32<128>(a, num_sms, st) : launch_f32<64>(a, num_sms, st);
 }

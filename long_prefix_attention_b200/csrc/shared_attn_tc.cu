@@ -1,0 +1,674 @@
+// shared_attn_tc.cu -- attention of a ragged batch over shared prefixes and
+// the rows' own pages on the tensor cores (bf16 storage).
+//
+// One CTA per SM takes one worker's range of the plan's units (128 keys of
+// one tile for one KV head) and works segment by segment: S = Q K^T and
+// O += P V on tcgen05.mma, fp32 accumulators in tensor memory, the softmax in
+// registers with a running maximum that is only raised when it grows by more
+// than 8 (base 2; numerator and denominator share it, so a stale maximum is
+// exact).  Warp roles:
+//   warp 0     producer: the page ids of a unit (one lane per page, read one
+//              unit ahead), then one TMA box per page and 64 columns, K and V
+//              tiles in turn through a ring that runs on across segments;
+//   warp 1     tensor memory; one lane issues the products; before the last
+//              tile's V is used it clears the places behind the last key, and
+//              the non-finite values of keys that some of the tile's rows do
+//              not see (0 times a NaN would reach them), noting those keys;
+//   warps 2-5  softmax stream 0, warps 6-9 softmax stream 1: a thread per
+//              query row (tensor-memory lane).
+// A tile of more than 128 rows gives each stream 128 of its rows and all keys
+// (one read of K and V serves 256 rows); a smaller one gives both streams the
+// same rows and every other unit of keys, so that in either case one stream's
+// softmax runs under the other's products.  The two states of a row are
+// joined in the epilogue.  Decode tiles with a few rows waste most of a
+// product, which costs nothing: a 128-key unit takes the tensor core 0.8 us
+// at most and 64 KB take an SM's share of HBM 1.5 us; warps without rows skip
+// the softmax.
+// Tensor memory columns: O_0 [0,128) O_1 [128,256) S_0 / P_0 [256,384)
+// S_1 / P_1 [384,512).  Products complete in issue order, so S_x(next) (issued
+// after P_x V) overwrites P_x only once it was read, and its completion means
+// that O_x is stable.  Every wait is bounded; a timeout ends the CTA's waits and
+// sets the error word.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "common.cuh"
+#include "launch.h"
+#include "shared.cuh"
+#include "umma.cuh"
+
+namespace asmk {
+namespace shared {
+namespace tc {
+
+using namespace umma;
+
+constexpr int kThreads = 320;
+constexpr int kSoftmax = 256;       // threads of the two softmax streams
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescale = 8.f;
+constexpr int kBox = 128 * 128;     // 128 rows x 64 columns of bf16
+constexpr int kFixUnits = 4;        // units of a tile that some of its rows see in part
+
+template <int D>
+struct Cfg {
+    static constexpr int HALVES = D / 64;
+    static constexpr int TILE = HALVES * kBox;
+    static constexpr int RING = D == 128 ? 4 : 8;   // K or V tiles in flight
+};
+
+template <int D>
+struct Smem {
+    unsigned char q[2][Cfg<D>::TILE];
+    unsigned char kv[Cfg<D>::RING][Cfg<D>::TILE];
+    float2 ml[2][128];                 // a row's (max, sum) in each stream
+    uint32_t fix[kFixUnits][4];        // keys whose V was cleared, from the first masked unit on
+    uint64_t kv_full[Cfg<D>::RING], kv_empty[Cfg<D>::RING];
+    uint64_t q_full, s_full[2], p_full[2], o_full[2], fix_full;
+    uint32_t tmem_base;
+};
+
+struct Maps {
+    CUtensorMap k, v;
+};
+
+__device__ __forceinline__ void set_error(int *err, asm_status s) { atomicExch(err, (int)s); }
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+
+// 2^t for two arguments on the FMA pipe: t = n + f, f in [-1/2, 1/2], 2^f by a
+// polynomial of degree 5 fitted to it there (relative error 1.6e-7), 2^n
+// added into the exponent.  t is clamped at -125.
+__device__ __forceinline__ uint64_t exp2_poly_x2(uint64_t t2) {
+    const uint64_t t = pack_f32x2(fmaxf(lo_f32(t2), -125.f), fmaxf(hi_f32(t2), -125.f));
+    const uint64_t y = add_f32x2(t, pack_f32x2(12582912.f, 12582912.f));   // 1.5 * 2^23: n in the low bits
+    const uint64_t n = add_f32x2(y, pack_f32x2(-12582912.f, -12582912.f));
+    const uint64_t f = fma_f32x2(n, pack_f32x2(-1.f, -1.f), t);
+    uint64_t p = fma_f32x2(pack_f32x2(0.001327647245f, 0.001327647245f), f, pack_f32x2(0.009675540961f, 0.009675540961f));
+    p = fma_f32x2(p, f, pack_f32x2(0.05550713092f, 0.05550713092f));
+    p = fma_f32x2(p, f, pack_f32x2(0.2402212024f, 0.2402212024f));
+    p = fma_f32x2(p, f, pack_f32x2(0.693146944f, 0.693146944f));
+    p = fma_f32x2(p, f, pack_f32x2(1.000000119f, 1.000000119f));
+    return pack_u32x2((uint32_t)p + ((uint32_t)y << 23), (uint32_t)(p >> 32) + ((uint32_t)(y >> 32) << 23));
+}
+
+// Barrier of the softmax warps; true if any of their threads passes true.
+__device__ __forceinline__ bool softmax_any(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, %2, p;\n"
+        " selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r) : "r"((uint32_t)v), "n"(kSoftmax) : "memory");
+    return r != 0;
+}
+
+// The segments of one worker, in order.  Every role walks them by itself; the
+// next tile's descriptor is read ahead.
+struct Seg {
+    Tile t;
+    int g, k, n;          // KV head, first unit, units
+    bool direct;          // no other segment or tile has keys of these tokens
+    long long prow;       // first partial row
+};
+struct Walk {
+    const AttnArgs &a;
+    const Header &h;
+    long long u, end;
+    int w, i;
+    Tile t, next;
+    __device__ Walk(const AttnArgs &a_, const Header &h_, int w_) : a(a_), h(h_), w(w_) {
+        u = (long long)w * h.upc;
+        end = min(h.W, u + h.upc);
+        i = 0;
+        if (u < end) {
+            i = a.first[w];
+            t = a.tiles[i];
+            next = a.tiles[min(i + 1, h.ntiles - 1)];
+        }
+    }
+    __device__ bool step(Seg &s) {
+        if (u >= end) return false;
+        while (u >= t.unit0 * a.Hkv + (long long)t.units * a.Hkv) {
+            ++i;
+            t = next;
+            next = a.tiles[min(i + 1, h.ntiles - 1)];
+        }
+        const long long t0 = t.unit0 * a.Hkv;
+        s.t = t;
+        s.g = (int)((u - t0) / t.units);
+        const long long c0 = t0 + (long long)s.g * t.units;
+        s.k = (int)(u - c0);
+        s.n = (int)min((long long)(t.units - s.k), end - u);
+        s.direct = (t.flags & kDirect) && s.n == t.units;
+        s.prow = partial_row(t, a.G, s.g, w - (int)(c0 / h.upc));
+        u += s.n;
+        return true;
+    }
+};
+
+// First unit (of the tile) that holds a key some row of the tile does not
+// see, when keys end at the row's own token; the tile's units if there is none.
+__device__ __forceinline__ int first_masked_unit(const Tile &t) {
+    return (t.flags & kLocal) ? min(max(t.base + 1, 0) / kUnitKeys, t.units) : t.units;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
+    using C = Cfg<D>;
+    constexpr int RING = C::RING;
+    extern __shared__ unsigned char smem_raw[];
+    Smem<D> &sm = *reinterpret_cast<Smem<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < RING; ++i) {
+            mbar_init(&sm.kv_full[i], 1);
+            mbar_init(&sm.kv_empty[i], 1);
+        }
+        mbar_init(&sm.q_full, kSoftmax);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&sm.s_full[x], 1);
+            mbar_init(&sm.p_full[x], 128);
+            mbar_init(&sm.o_full[x], 1);
+        }
+        mbar_init(&sm.fix_full, 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_addr(&sm.tmem_base)), "r"(kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    const Header h = *a.hdr;
+    const bool fits = plan_ok(a, h);
+    if (!fits && blockIdx.x == 0 && tid == 0) set_error(a.ws_err, ASM_ERR_INVALID_ARG);
+    const int w = blockIdx.x;
+    bool ok = true;
+    // the lanes of a warp agree on a timeout, so that none leaves the others in a collective
+    auto wait = [&](uint64_t *bar, uint32_t parity) { ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity)); };
+
+    if (!fits || w >= h.workers) {
+        // nothing to do for this CTA
+    } else if (warp == 0) {
+        // ------------------------------------------------------ producer
+        const int rows = min(a.S, kUnitKeys), boxes = kUnitKeys / rows;  // keys and boxes per page of a unit
+        Walk walk(a, h, w);
+        Seg s;
+        uint32_t n = 0;            // ring items so far
+        while (walk.step(s)) {
+            const int *list = (s.t.flags & kLocal) ? a.table + (size_t)s.t.owner * a.max_pages
+                                                   : a.prefix_table + (size_t)s.t.owner * a.max_prefix_pages;
+            auto page = [&](int unit) {     // this lane's page of a unit
+                const int key = unit * kUnitKeys + lane * rows;
+                return (lane < boxes && unit < s.k + s.n && key < s.t.keys) ? list[key >> a.shift] : -1;
+            };
+            int ahead = page(s.k);
+            for (int j = s.k; j < s.k + s.n; ++j) {
+                const int id = ahead;
+                ahead = page(j + 1);
+                const bool used = lane < boxes && j * kUnitKeys + lane * rows < s.t.keys;
+                const bool bad = used && (id < 0 || id >= a.n_pages);
+                if (bad) set_error(a.ws_err, ASM_ERR_INVALID_ARG);
+                // past the cache (zero fill) for places behind the last key and bad ids
+                const int c2 = used && !bad ? id * a.Hkv + s.g : a.n_pages * a.Hkv;
+                for (int kv = 0; kv < 2; ++kv, ++n) {
+                    const int slot = n % RING;
+                    if (n >= RING) wait(&sm.kv_empty[slot], ((n / RING) - 1) & 1);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&sm.kv_full[slot], C::TILE);
+                    __syncwarp();
+                    if (lane < boxes) {
+#pragma unroll
+                        for (int hf = 0; hf < C::HALVES; ++hf)
+                            tma_load_3d(sm.kv[slot] + hf * kBox + lane * rows * 128, kv ? &maps.v : &maps.k, 64 * hf, 0, c2,
+                                        &sm.kv_full[slot]);
+                    }
+                }
+                if (!ok) break;
+            }
+            if (!ok) break;
+        }
+        // every copy that was issued has landed before the CTA may end
+        for (uint32_t i = n > RING ? n - RING : 0; i < n; ++i)
+            if (!mbar_wait(&sm.kv_full[i % RING], (i / RING) & 1)) ok = false;
+    } else if (warp == 1) {
+        // ------------------------------------------------- MMA issuer
+        const uint32_t idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kUnitKeys >> 3) << 17) |
+                                 ((uint32_t)(128 >> 4) << 24);
+        const uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
+                                 ((uint32_t)(128 >> 4) << 24);
+        Walk walk(a, h, w);
+        Seg s;
+        uint32_t base = 0;         // ring item of the segment's first K
+        uint32_t pn[2] = {0, 0};   // P tiles taken from each stream
+        uint32_t segs = 0;
+        auto slot_of = [&](uint32_t item) { return item % RING; };
+        auto wait_kv = [&](uint32_t item) { wait(&sm.kv_full[slot_of(item)], (item / RING) & 1); };
+        while (ok && walk.step(s)) {
+            const bool dual = s.t.ntok * a.G > kTileRows;
+            const int n = s.n;
+            const int masked = first_masked_unit(s.t);
+            auto issue_s = [&](int x, uint32_t item) {
+                if (lane == 0) {
+                    const uint32_t qb = smem_addr(sm.q[dual ? x : 0]), kb = smem_addr(sm.kv[slot_of(item)]);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (uint32_t)((kk >> 2) * kBox + (kk & 3) * 32);
+                        umma_bf16(tmem + 256 + (uint32_t)(x * 128), desc_k_sw128(qb + off), desc_k_sw128(kb + off),
+                                  idesc_s, kk > 0 ? 1u : 0u);
+                    }
+                    umma_commit(&sm.s_full[x]);
+                }
+            };
+            auto issue_pv = [&](int x, uint32_t item, bool first) {
+                if (lane == 0) {
+                    const uint32_t vb = smem_addr(sm.kv[slot_of(item)]);
+#pragma unroll
+                    for (int kk = 0; kk < kUnitKeys / 16; ++kk)
+                        umma_bf16_ts(tmem + (uint32_t)(x * 128), tmem + 256 + (uint32_t)(x * 128 + kk * 8),
+                                     desc_mn_sw128(vb + (uint32_t)(kk * 2048), kBox), idesc_o,
+                                     (!first || kk > 0) ? 1u : 0u);
+                }
+            };
+            auto commit = [&](uint64_t *bar) {
+                if (lane == 0) umma_commit(bar);
+            };
+            // V of unit s.k + j as the products may use it
+            auto clean = [&](int j, uint32_t item) {
+                const int unit = s.k + j, key0 = unit * kUnitKeys, valid = s.t.keys - key0;
+                if (unit < masked && valid >= kUnitKeys) return;
+                unsigned char *v = sm.kv[slot_of(item)];
+                if (unit >= masked) {
+                    const int r0 = max(s.t.base + 1 - key0, 0), r1 = min(valid, kUnitKeys);
+                    for (int c = lane; c < (r1 - r0) * (D / 8); c += 32) {
+                        const int r = r0 + c / (D / 8), cc = c % (D / 8);
+                        uint4 *p = reinterpret_cast<uint4 *>(v + (cc >> 3) * kBox + swz128(r, cc & 7));
+                        uint4 x = *p;
+                        uint32_t *e = reinterpret_cast<uint32_t *>(&x);
+                        bool bad = false;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if ((e[i] & 0x7f80u) == 0x7f80u) { e[i] &= 0xffff0000u; bad = true; }
+                            if ((e[i] & 0x7f800000u) == 0x7f800000u) { e[i] &= 0xffffu; bad = true; }
+                        }
+                        if (bad) {
+                            *p = x;
+                            atomicOr(&sm.fix[min(unit - masked, kFixUnits - 1)][r >> 5], 1u << (r & 31));
+                        }
+                    }
+                }
+                if (valid < kUnitKeys) {
+                    for (int c = lane; c < (kUnitKeys - valid) * (D / 8); c += 32) {
+                        const int r = valid + c / (D / 8), cc = c % (D / 8);
+                        *reinterpret_cast<uint4 *>(v + (cc >> 3) * kBox + swz128(r, cc & 7)) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+            };
+            auto item_k = [&](int j) { return base + 2 * (uint32_t)j; };
+            auto item_v = [&](int j) { return base + 2 * (uint32_t)j + 1; };
+
+            wait(&sm.q_full, segs & 1);
+            if (dual) {
+                wait_kv(item_k(0));
+                tc_fence_after();
+                issue_s(0, item_k(0));
+                issue_s(1, item_k(0));
+                commit(&sm.kv_empty[slot_of(item_k(0))]);
+                for (int j = 0; j < n && ok; ++j) {
+                    const bool more = j + 1 < n;
+                    wait_kv(item_v(j));
+                    clean(j, item_v(j));
+                    if (!more && lane == 0) mbar_arrive(&sm.fix_full);
+                    for (int x = 0; x < 2; ++x) {
+                        wait(&sm.p_full[x], pn[x] & 1);
+                        ++pn[x];
+                        tc_fence_after();
+                        issue_pv(x, item_v(j), j == 0);
+                        if (more) {
+                            if (x == 0) wait_kv(item_k(j + 1));
+                            issue_s(x, item_k(j + 1));
+                        } else {
+                            commit(&sm.o_full[x]);
+                        }
+                    }
+                    commit(&sm.kv_empty[slot_of(item_v(j))]);
+                    if (more) commit(&sm.kv_empty[slot_of(item_k(j + 1))]);
+                }
+            } else {
+                for (int j = 0; j < min(n, 2); ++j) {
+                    wait_kv(item_k(j));
+                    tc_fence_after();
+                    issue_s(j, item_k(j));
+                    commit(&sm.kv_empty[slot_of(item_k(j))]);
+                }
+                for (int j = 0; j < n && ok; ++j) {
+                    const int x = j & 1;
+                    wait_kv(item_v(j));
+                    clean(j, item_v(j));
+                    if (j == n - 1 && lane == 0) mbar_arrive(&sm.fix_full);
+                    wait(&sm.p_full[x], pn[x] & 1);
+                    ++pn[x];
+                    tc_fence_after();
+                    issue_pv(x, item_v(j), j < 2);
+                    commit(&sm.kv_empty[slot_of(item_v(j))]);
+                    if (j + 2 < n) {
+                        wait_kv(item_k(j + 2));
+                        issue_s(x, item_k(j + 2));
+                        commit(&sm.kv_empty[slot_of(item_k(j + 2))]);
+                    } else {
+                        commit(&sm.o_full[x]);
+                    }
+                }
+            }
+            base += 2 * (uint32_t)n;
+            ++segs;
+        }
+        __syncwarp();
+    } else {
+        // ----------------------------------------------------- softmax
+        const int x = (warp - 2) >> 2;      // stream
+        const int qd = warp & 3;            // tensor-memory lane quarter
+        const int row = qd * 32 + lane;     // row within the stream's 128
+        const int st = tid - 64;            // thread among the softmax threads
+        const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
+        const uint32_t t_s = tmem + lane_off + 256 + (uint32_t)(x * 128);
+        const float sl2 = a.sl2;
+        Walk walk(a, h, w);
+        Seg s;
+        uint32_t sn = 0, on[2] = {0, 0}, segs = 0;
+        while (walk.step(s)) {
+            const int rows = s.t.ntok * a.G;
+            const bool dual = rows > kTileRows, local = s.t.flags & kLocal;
+            // ---- the tile's queries into the swizzled operand layout
+            {
+                const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) +
+                                         ((size_t)s.t.tok0 * a.Hq + (size_t)s.g * a.G) * D;
+                constexpr int CH = D / 8;
+#pragma unroll 4
+                for (int i = st; i < rows * CH; i += kSoftmax) {
+                    const int r = i / CH, c = i - r * CH, tk = r / a.G, hh = r - tk * a.G;
+                    const uint4 v = *reinterpret_cast<const uint4 *>(q + ((size_t)tk * a.Hq + hh) * D + c * 8);
+                    *reinterpret_cast<uint4 *>(sm.q[r >> 7] + (c >> 3) * kBox + swz128(r & 127, c & 7)) = v;
+                }
+                if (st < kFixUnits * 4) sm.fix[st >> 2][st & 3] = 0;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                mbar_arrive(&sm.q_full);
+            }
+            const int first = dual ? 0 : x, step = dual ? 1 : 2;
+            const int r = dual ? x * 128 + row : row;       // row of the tile
+            const bool live = r < rows;
+            const bool warp_live = (dual ? x * 128 : 0) + qd * 32 < rows;
+            const int tk = r / a.G;
+            const int lim = live ? (local ? min(s.t.base + tk + 1, s.t.keys) : s.t.keys) : s.t.keys;
+            float m_used = kNegInf, l = 0.f;
+            int j = first;
+            for (; j < s.n; j += step) {
+                wait(&sm.s_full[x], sn & 1);
+                ++sn;
+                if (!ok) break;
+                tc_fence_after();
+                if (warp_live) {
+                    const int vis = lim - (s.k + j) * kUnitKeys;   // keys of this unit the row sees
+                    const bool part = __any_sync(0xffffffffu, vis < kUnitKeys);
+                    float mraw = kNegInf;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32(t_s + (uint32_t)(32 * c), v);
+                        tmem_wait_ld();
+                        if (part) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (32 * c + i >= vis) v[i] = 0xff800000u;  // -inf
+                        }
+                        float m11[11];
+#pragma unroll
+                        for (int i = 0; i < 10; ++i)
+                            m11[i] = max3_nan(__uint_as_float(v[3 * i]), __uint_as_float(v[3 * i + 1]),
+                                              __uint_as_float(v[3 * i + 2]));
+                        m11[10] = max_nan(__uint_as_float(v[30]), __uint_as_float(v[31]));
+                        mraw = max3_nan(mraw, max3_nan(max3_nan(m11[0], m11[1], m11[2]), max3_nan(m11[3], m11[4], m11[5]),
+                                                       max3_nan(m11[6], m11[7], m11[8])), max_nan(m11[9], m11[10]));
+                    }
+                    const float mt = mraw * sl2;
+                    float alpha = 1.f;
+                    if (live && !(mt <= m_used + kRescale)) {   // a NaN passes, and stays
+                        alpha = ex2f(m_used - mt);
+                        m_used = mt;
+                        l *= alpha;
+                    }
+                    // tensor-memory access is warp-wide: rows that keep their maximum scale by 1
+                    if (j > first && __any_sync(0xffffffffu, alpha != 1.f)) {
+                        const uint32_t t_o = tmem + lane_off + (uint32_t)(x * 128);
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(t_o + (uint32_t)c0, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            tmem_st32(t_o + (uint32_t)c0, o);
+                        }
+                    }
+                    // p = 2^(s scale log2(e) - m), rounded to bf16 for the product with V
+                    // (the sum keeps fp32); P goes over columns of S already read
+                    const float ref = m_used == kNegInf ? 0.f : m_used;
+                    const uint64_t sl2x2 = pack_f32x2(sl2, sl2), negm2 = pack_f32x2(-ref, -ref);
+                    uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32(t_s + (uint32_t)(32 * c), v);
+                        tmem_wait_ld();
+                        uint32_t pk[16];
+                        if (part) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (32 * c + i >= vis) v[i] = 0xff800000u;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const uint64_t t2 = fma_f32x2(pack_u32x2(v[2 * i], v[2 * i + 1]), sl2x2, negm2);
+                                const uint64_t p2 = pack_f32x2(ex2f(lo_f32(t2)), ex2f(hi_f32(t2)));
+                                acc[i & 3] = add_f32x2(acc[i & 3], p2);
+                                pk[i] = pack_bf16(lo_f32(p2), hi_f32(p2));
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const uint64_t t2 = fma_f32x2(pack_u32x2(v[2 * i], v[2 * i + 1]), sl2x2, negm2);
+                                uint64_t p2;
+                                if ((i & 3) == 3) p2 = exp2_poly_x2(t2);
+                                else p2 = pack_f32x2(ex2f(lo_f32(t2)), ex2f(hi_f32(t2)));
+                                acc[i & 3] = add_f32x2(acc[i & 3], p2);
+                                pk[i] = pack_bf16(lo_f32(p2), hi_f32(p2));
+                            }
+                        }
+                        tmem_st16(t_s + (uint32_t)(16 * c), pk);
+                    }
+                    const uint64_t a01 = add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3]));
+                    l += lo_f32(a01) + hi_f32(a01);
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                mbar_arrive(&sm.p_full[x]);
+            }
+            // ------------------------------------------------------ epilogue
+            // the streams that had units (a small tile of one unit has only the first)
+            const bool two = dual || s.n > 1;
+            if (!dual) {
+                sm.ml[x][row] = make_float2(m_used, l);
+                wait(&sm.o_full[0], on[0] & 1);
+                ++on[0];
+                if (two) {
+                    wait(&sm.o_full[1], on[1] & 1);
+                    ++on[1];
+                }
+            } else {
+                wait(&sm.o_full[x], on[x] & 1);
+                ++on[0];
+                ++on[1];
+            }
+            wait(&sm.fix_full, segs & 1);
+            ok = !softmax_any(!ok);   // all eight warps go on or none
+            tc_fence_after();
+            if (!ok) break;
+            if (warp_live) {
+                float w0 = 1.f, w1 = 0.f, m = m_used;
+                if (!dual) {
+                    const float2 s0 = sm.ml[0][row], s1 = sm.ml[1][row];
+                    m = two ? max_nan(s0.x, s1.x) : s0.x;
+                    const float ref = m == kNegInf ? 0.f : m;
+                    w0 = ex2f(s0.x - ref);
+                    w1 = two ? ex2f(s1.x - ref) : 0.f;
+                    l = two ? w0 * s0.y + w1 * s1.y : w0 * s0.y;
+                }
+                const size_t th = (size_t)(s.t.tok0 + tk) * a.Hq + (size_t)s.g * a.G + (r - tk * a.G);
+                const float inv = s.direct ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+                // a small tile's streams each write half of the columns
+                const int c_lo = dual ? 0 : x * (D / 2), c_hi = dual ? D : c_lo + D / 2;
+                const uint32_t t_o = tmem + lane_off + (dual ? (uint32_t)(x * 128) : 0u);
+                const int masked = first_masked_unit(s.t);
+#pragma unroll 1
+                for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(t_o + (uint32_t)c0, o);
+                    tmem_wait_ld();
+                    if (!dual) {
+                        // a stream that saw no key of the row holds no value for it
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = w0 == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * w0);
+                        if (two) {
+                            uint32_t o1[32];
+                            tmem_ld32(t_o + 128u + (uint32_t)c0, o1);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (w1 != 0.f)
+                                    o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), w1, __uint_as_float(o[i])));
+                        }
+                    }
+                    if (masked < s.k + s.n && live) {
+                        // non-finite values of keys that only some rows see: back into the rows that do
+                        for (int fu = 0; fu < kFixUnits; ++fu) {
+                            for (int b = 0; b < 4; ++b) {
+                                uint32_t bits = sm.fix[fu][b];
+                                while (bits) {
+                                    const int key = (masked + fu) * kUnitKeys + 32 * b + __ffs(bits) - 1;
+                                    bits &= bits - 1;
+                                    if (key >= lim) continue;
+                                    const int id = a.table[(size_t)s.t.owner * a.max_pages + (key >> a.shift)];
+                                    if (id < 0 || id >= a.n_pages) continue;
+                                    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v_pages) +
+                                        ((((long long)id * a.Hkv + s.g) << a.shift) + (key & (a.S - 1))) * D + c0;
+#pragma unroll 1
+                                    for (int i = 0; i < 32; ++i) {
+                                        const float f = __bfloat162float(v[i]);
+                                        if (!(f - f == 0.f)) {
+#pragma unroll
+                                            for (int e = 0; e < 32; ++e)
+                                                if (e == i) o[e] = __float_as_uint(__uint_as_float(o[e]) + f);
+                                        }
+                                    }
+                                }
+                            }
+                        }
+                    }
+                    if (live) {
+                        if (s.direct) {
+                            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + th * D + c0;
+#pragma unroll
+                            for (int i = 0; i < 32; i += 8) {
+                                uint32_t pk[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    pk[e] = pack_bf16(__uint_as_float(o[i + 2 * e]) * inv,
+                                                      __uint_as_float(o[i + 2 * e + 1]) * inv);
+                                *reinterpret_cast<uint4 *>(dst + i) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                            }
+                        } else {
+                            float *dst = a.ws_o + (size_t)(s.prow + r) * D + c0;
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4)
+                                *reinterpret_cast<uint4 *>(dst + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        }
+                    }
+                }
+                if (live && (dual || x == 0)) {
+                    if (!s.direct) a.ws_ml[s.prow + r] = make_float2(m, l);
+                    else if (a.lse) a.lse[th] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+                }
+            }
+            tc_fence_before();
+            asm volatile("bar.sync 1, %0;" ::"n"(kSoftmax) : "memory");
+            ++segs;
+        }
+    }
+    if (!ok && lane == 0) set_error(a.ws_err, ASM_ERR_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+    }
+}
+
+}  // namespace tc
+}  // namespace shared
+
+bool make_map_3d(CUtensorMap *m, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t rows);
+
+namespace shared {
+
+template <int D>
+cudaError_t launch_tc(const AttnArgs &a, int num_sms, cudaStream_t st) {
+    tc::Maps maps;
+    memset(&maps, 0, sizeof(maps));
+    const uint64_t heads = (uint64_t)a.n_pages * a.Hkv;
+    const uint32_t box = (uint32_t)(a.S < kUnitKeys ? a.S : kUnitKeys);
+    if (!make_map_3d(&maps.k, a.k_pages, D, a.S, heads, box) || !make_map_3d(&maps.v, a.v_pages, D, a.S, heads, box))
+        return cudaErrorInvalidValue;
+    auto kern = tc::shared_attn_tc_kernel<D>;
+    const size_t smem = sizeof(tc::Smem<D>) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.workers);
+    cfg.blockDim = dim3(tc::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, maps, a);
+}
+
+cudaError_t launch_attn_tc(const AttnArgs &a, int num_sms, cudaStream_t st) {
+    return a.d == 128 ? launch_tc<128>(a, num_sms, st) : launch_tc<64>(a, num_sms, st);
+}
+
+}  // namespace shared
+}  // namespace asmk

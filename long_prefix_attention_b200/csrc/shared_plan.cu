@@ -16,7 +16,6 @@ namespace asmk {
 namespace shared {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPer = kMaxRows / kPlanThreads;
 
 struct PlanArgs {
     const int *q_off, *seq_len, *group_off, *prefix_len;
