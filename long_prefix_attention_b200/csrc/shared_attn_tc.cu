@@ -10,12 +10,13 @@
 //   warp 0     producer: the page ids of a unit (one lane per page, read one
 //              unit ahead), then one TMA box per page and 64 columns, K and V
 //              tiles in turn through a ring that runs on across segments;
-//   warp 1     tensor memory; one lane issues the products; before the last
-//              tile's V is used it clears the places behind the last key, and
-//              the non-finite values of keys that some of the tile's rows do
-//              not see (0 times a NaN would reach them), noting those keys;
+//   warp 1     tensor memory; one lane issues the products;
 //   warps 2-5  softmax stream 0, warps 6-9 softmax stream 1: a thread per
-//              query row (tensor-memory lane).
+//              query row (tensor-memory lane).  In units that end a tile's
+//              keys they also clear the places of V behind the last key, and
+//              the non-finite values of keys that some of the tile's rows do
+//              not see (0 times a NaN would reach those rows); the epilogue
+//              adds them back to the rows that do.
 // A tile of more than 128 rows gives each stream 128 of its rows and all keys
 // (one read of K and V serves 256 rows); a smaller one gives both streams the
 // same rows and every other unit of keys, so that in either case one stream's
@@ -67,7 +68,7 @@ struct Smem {
     float2 ml[2][128];                 // a row's (max, sum) in each stream
     uint32_t fix[kFixUnits][4];        // keys whose V was cleared, from the first masked unit on
     uint64_t kv_full[Cfg<D>::RING], kv_empty[Cfg<D>::RING];
-    uint64_t q_full, s_full[2], p_full[2], o_full[2], fix_full;
+    uint64_t q_full, s_full[2], p_full[2], o_full[2];
     uint32_t tmem_base;
 };
 
@@ -164,6 +165,37 @@ __device__ __forceinline__ int first_masked_unit(const Tile &t) {
     return (t.flags & kLocal) ? min(max(t.base + 1, 0) / kUnitKeys, t.units) : t.units;
 }
 
+// Clears the places [r1, 128) of a V tile, and the non-finite values of keys
+// [r0, r1), whose bits are set in `fix`; 128 threads.
+template <int D>
+__device__ __forceinline__ void clean_values(unsigned char *v, int r0, int r1, int thread, uint32_t *fix) {
+    constexpr int CH = D / 8;
+    for (int c = thread; c < (r1 - r0) * CH; c += 128) {
+        const int r = r0 + c / CH, cc = c % CH;
+        uint4 *p = reinterpret_cast<uint4 *>(v + (cc >> 3) * kBox + swz128(r, cc & 7));
+        const uint4 x = *p;
+        // bf16 exponents of all ones, in the halves of four words
+        uint32_t y[4] = {x.x, x.y, x.z, x.w};
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = (y[i] & 0x7f80u) == 0x7f80u ? 0xffffu : 0u;
+            const uint32_t hi = (y[i] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u;
+            bad |= (lo | hi) != 0u;
+            y[i] &= ~(lo | hi);
+        }
+        if (bad) {
+            *p = make_uint4(y[0], y[1], y[2], y[3]);
+            atomicOr(&fix[r >> 5], 1u << (r & 31));
+        }
+    }
+    for (int c = thread; c < (kUnitKeys - r1) * CH; c += 128) {
+        const int r = r1 + c / CH, cc = c % CH;
+        *reinterpret_cast<uint4 *>(v + (cc >> 3) * kBox + swz128(r, cc & 7)) = make_uint4(0, 0, 0, 0);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
@@ -184,7 +216,6 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
             mbar_init(&sm.p_full[x], 128);
             mbar_init(&sm.o_full[x], 1);
         }
-        mbar_init(&sm.fix_full, 1);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -267,7 +298,6 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
         while (ok && walk.step(s)) {
             const bool dual = s.t.ntok * a.G > kTileRows;
             const int n = s.n;
-            const int masked = first_masked_unit(s.t);
             auto issue_s = [&](int x, uint32_t item) {
                 if (lane == 0) {
                     const uint32_t qb = smem_addr(sm.q[dual ? x : 0]), kb = smem_addr(sm.kv[slot_of(item)]);
@@ -293,39 +323,6 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
             auto commit = [&](uint64_t *bar) {
                 if (lane == 0) umma_commit(bar);
             };
-            // V of unit s.k + j as the products may use it
-            auto clean = [&](int j, uint32_t item) {
-                const int unit = s.k + j, key0 = unit * kUnitKeys, valid = s.t.keys - key0;
-                if (unit < masked && valid >= kUnitKeys) return;
-                unsigned char *v = sm.kv[slot_of(item)];
-                if (unit >= masked) {
-                    const int r0 = max(s.t.base + 1 - key0, 0), r1 = min(valid, kUnitKeys);
-                    for (int c = lane; c < (r1 - r0) * (D / 8); c += 32) {
-                        const int r = r0 + c / (D / 8), cc = c % (D / 8);
-                        uint4 *p = reinterpret_cast<uint4 *>(v + (cc >> 3) * kBox + swz128(r, cc & 7));
-                        uint4 x = *p;
-                        uint32_t *e = reinterpret_cast<uint32_t *>(&x);
-                        bool bad = false;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if ((e[i] & 0x7f80u) == 0x7f80u) { e[i] &= 0xffff0000u; bad = true; }
-                            if ((e[i] & 0x7f800000u) == 0x7f800000u) { e[i] &= 0xffffu; bad = true; }
-                        }
-                        if (bad) {
-                            *p = x;
-                            atomicOr(&sm.fix[min(unit - masked, kFixUnits - 1)][r >> 5], 1u << (r & 31));
-                        }
-                    }
-                }
-                if (valid < kUnitKeys) {
-                    for (int c = lane; c < (kUnitKeys - valid) * (D / 8); c += 32) {
-                        const int r = valid + c / (D / 8), cc = c % (D / 8);
-                        *reinterpret_cast<uint4 *>(v + (cc >> 3) * kBox + swz128(r, cc & 7)) = make_uint4(0, 0, 0, 0);
-                    }
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-            };
             auto item_k = [&](int j) { return base + 2 * (uint32_t)j; };
             auto item_v = [&](int j) { return base + 2 * (uint32_t)j + 1; };
 
@@ -339,8 +336,6 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 for (int j = 0; j < n && ok; ++j) {
                     const bool more = j + 1 < n;
                     wait_kv(item_v(j));
-                    clean(j, item_v(j));
-                    if (!more && lane == 0) mbar_arrive(&sm.fix_full);
                     for (int x = 0; x < 2; ++x) {
                         wait(&sm.p_full[x], pn[x] & 1);
                         ++pn[x];
@@ -366,8 +361,6 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 for (int j = 0; j < n && ok; ++j) {
                     const int x = j & 1;
                     wait_kv(item_v(j));
-                    clean(j, item_v(j));
-                    if (j == n - 1 && lane == 0) mbar_arrive(&sm.fix_full);
                     wait(&sm.p_full[x], pn[x] & 1);
                     ++pn[x];
                     tc_fence_after();
@@ -397,7 +390,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
         const float sl2 = a.sl2;
         Walk walk(a, h, w);
         Seg s;
-        uint32_t sn = 0, on[2] = {0, 0}, segs = 0;
+        uint32_t sn = 0, on[2] = {0, 0}, base = 0;   // base: ring item of the segment's first K
         while (walk.step(s)) {
             const int rows = s.t.ntok * a.G;
             const bool dual = rows > kTileRows, local = s.t.flags & kLocal;
@@ -421,6 +414,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
             const bool live = r < rows;
             const bool warp_live = (dual ? x * 128 : 0) + qd * 32 < rows;
             const int tk = r / a.G;
+            const int masked = first_masked_unit(s.t);
             const int lim = live ? (local ? min(s.t.base + tk + 1, s.t.keys) : s.t.keys) : s.t.keys;
             float m_used = kNegInf, l = 0.f;
             int j = first;
@@ -511,6 +505,17 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                     l += lo_f32(a01) + hi_f32(a01);
                     tmem_wait_st();
                 }
+                const int unit = s.k + j, valid = s.t.keys - unit * kUnitKeys;
+                if (unit >= masked || valid < kUnitKeys) {
+                    // V as the product may use it (both streams of a tall tile do the same)
+                    const uint32_t item = base + 2 * (uint32_t)j + 1;
+                    wait(&sm.kv_full[item % RING], (item / RING) & 1);
+                    if (ok) {
+                        unsigned char *v = sm.kv[item % RING];
+                        const int r0 = unit >= masked ? max(s.t.base + 1 - unit * kUnitKeys, 0) : kUnitKeys;
+                        clean_values<D>(v, r0, min(valid, kUnitKeys), row, sm.fix[min(max(unit - masked, 0), kFixUnits - 1)]);
+                    }
+                }
                 tc_fence_before();
                 mbar_arrive(&sm.p_full[x]);
             }
@@ -530,7 +535,6 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 ++on[0];
                 ++on[1];
             }
-            wait(&sm.fix_full, segs & 1);
             ok = !softmax_any(!ok);   // all eight warps go on or none
             tc_fence_after();
             if (!ok) break;
@@ -549,7 +553,6 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 // a small tile's streams each write half of the columns
                 const int c_lo = dual ? 0 : x * (D / 2), c_hi = dual ? D : c_lo + D / 2;
                 const uint32_t t_o = tmem + lane_off + (dual ? (uint32_t)(x * 128) : 0u);
-                const int masked = first_masked_unit(s.t);
 #pragma unroll 1
                 for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
                     uint32_t o[32];
@@ -622,7 +625,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
             }
             tc_fence_before();
             asm volatile("bar.sync 1, %0;" ::"n"(kSoftmax) : "memory");
-            ++segs;
+            base += 2 * (uint32_t)s.n;
         }
     }
     if (!ok && lane == 0) set_error(a.ws_err, ASM_ERR_TIMEOUT);
