@@ -4,12 +4,13 @@
 // A tile is a run of tokens of one row (its local pages) or of one prefix
 // group (the group's prefix pages) with the G query heads of a KV head: at
 // most 128 query rows, or 256 when the run is longer than that.  A unit is
-// 128 keys of one tile for one KV head.  The units of all (tile, KV head)
-// pairs form one sequence, tile by tile and head by head, which is cut into
-// equal ranges, one per worker (CTA): the work is balanced whatever the
-// lengths are, and a long key list is split as far as there are workers.  A
-// pair whose units fall to several workers leaves one partial state per
-// worker (a segment); the merge kernel joins them.
+// 128 keys of one tile for one KV head.  The (tile, KV head) pairs, tile by
+// tile and head by head, are laid end to end by their cost and the line is
+// cut into equal ranges, one per worker (CTA): the work is balanced whatever
+// the lengths are, and a long key list is split as far as there are workers.
+// A worker takes the units that begin in its range; a pair whose units fall
+// to several workers leaves one partial state per worker (a segment), which
+// the merge kernel joins.
 #pragma once
 
 #include <stdint.h>
@@ -30,16 +31,26 @@ struct __align__(16) Tile {
     int base;          // local: keys that lie before the token tok0 itself
     int units;         // ceil(keys / kUnitKeys)
     int cap;           // segments at most, per KV head
-    long long unit0;   // units of all tiles before, times one KV head
+    long long cost0;   // cost of all tiles before, for one KV head
     long long row0;    // partial rows of all tiles before
 };
 constexpr int kLocal = 1;   // keys in the row's own pages, causal
 constexpr int kDirect = 2;  // the tile holds all keys of its tokens
 
+// Cost of a tile for one KV head: COST_HEAD for its queries and its epilogue,
+// then so much per unit.  A 256-row unit costs about twice a 128-row one (the
+// tensor cores against HBM).
+constexpr int kCostMax = 4;
+__host__ __device__ inline int cost_unit(int rows) { return rows > kTileRows ? 4 : 2; }
+__host__ __device__ inline int cost_head(int rows) { return rows > kTileRows ? 4 : 3; }
+__host__ __device__ inline long long cost_of(int rows, int units) {
+    return units > 0 ? cost_head(rows) + (long long)cost_unit(rows) * units : 0;
+}
+
 struct Header {
     int magic, R, NG, T, Hq, Hkv, page_size, max_pages, max_prefix_pages, workers, ntiles;
-    int upc;           // units per worker
-    long long W;       // units of all (tile, KV head) pairs
+    int range;         // cost per worker
+    long long W;       // cost of all (tile, KV head) pairs
 };
 
 // Byte offsets in the plan buffer.
@@ -61,8 +72,8 @@ inline __host__ __device__ PlanLayout plan_layout(int R, int NG, int T, int G) {
     return p;
 }
 
-// Partial rows: every (tile, KV head) pair has at most 2 + units / upc
-// segments of its rows, and the units / upc sum to at most the workers.
+// Partial rows: every (tile, KV head) pair has at most 2 + cost / range
+// segments of its rows, and the cost / range sum to at most the workers.
 inline __host__ __device__ long long max_partial_rows(int T, int Hq, int workers) {
     return 4LL * T * Hq + (long long)(workers + 1) * kDualRows;
 }
@@ -103,15 +114,77 @@ __device__ __forceinline__ bool plan_ok(const AttnArgs &a, const Header &h) {
            h.page_size == a.S && h.workers == a.workers && h.max_pages == a.max_pages && h.max_prefix_pages == a.max_prefix_pages;
 }
 
-// Segments of the units [c0, c0 + n) when every worker has upc.
-__device__ __forceinline__ int segments(long long c0, int n, int upc) {
-    return n > 0 ? (int)((c0 + n - 1) / upc - c0 / upc) + 1 : 0;
+// Worker that has the unit k of a pair whose cost begins at c0.
+__device__ __forceinline__ int worker_of(long long c0, int rows, int k, int range) {
+    return (int)((c0 + cost_head(rows) + (long long)cost_unit(rows) * k) / range);
+}
+// Segments of a pair.
+__device__ __forceinline__ int segments(long long c0, int rows, int units, int range) {
+    return units > 0 ? worker_of(c0, rows, units - 1, range) - worker_of(c0, rows, 0, range) + 1 : 0;
 }
 
-// First partial row of segment s of (tile, g).
-__device__ __forceinline__ long long partial_row(const Tile &t, int G, int g, int s) {
-    return t.row0 + ((long long)g * t.cap + s) * ((long long)t.ntok * G);
+// Partial states: the statistics of a segment's rows follow one another; its
+// outputs are stored 4 columns of all rows at a time, so that threads that
+// hold one row each write together: element (row, column).
+__device__ __forceinline__ size_t partial_at(long long first_row, int rows, int row, int col, int D) {
+    return (size_t)first_row * D + ((size_t)(col >> 2) * rows + row) * 4 + (col & 3);
 }
+
+// The segments of one worker, in order; the next tile's descriptor is read ahead.
+struct Seg {
+    Tile t;
+    int g, k, n;          // KV head, first unit, units
+    bool direct;          // no other segment or tile has keys of these tokens
+    long long prow;       // first partial row
+};
+struct Walk {
+    long long c, end;     // cost: where the current pair begins, where the range ends
+    int w, i, g, range, last, Hkv, G;
+    const Tile *tiles;
+    Tile t, next;
+    __device__ Walk(const AttnArgs &a, const Header &h, int w_)
+        : w(w_), g(0), range(h.range), last(h.ntiles - 1), Hkv(a.Hkv), G(a.G), tiles(a.tiles) {
+        const long long begin = (long long)w * range;
+        end = min(h.W, begin + range);
+        c = end;
+        i = 0;
+        if (begin < end) {
+            i = a.first[w];
+            t = tiles[i];
+            next = tiles[min(i + 1, last)];
+            const long long per = cost_of(t.ntok * G, t.units);
+            g = (int)((begin - t.cost0 * Hkv) / per);
+            c = t.cost0 * Hkv + g * per;
+        }
+    }
+    __device__ bool step(Seg &s) {
+        while (c < end) {
+            const int rows = t.ntok * G, cu = cost_unit(rows);
+            const long long u0 = c + cost_head(rows), lo = (long long)w * range;
+            // units that begin within [lo, end)
+            const int k0 = lo <= u0 ? 0 : (int)((lo - u0 + cu - 1) / cu);
+            const int k1 = t.units == 0 || end <= u0 ? 0 : (int)min((long long)t.units, (end - u0 + cu - 1) / cu);
+            const bool some = k0 < k1;
+            if (some) {
+                s.t = t;
+                s.g = g;
+                s.k = k0;
+                s.n = k1 - k0;
+                s.direct = (t.flags & kDirect) && s.n == t.units;
+                s.prow = t.row0 + ((long long)g * t.cap + (w - worker_of(c, rows, 0, range))) * rows;
+            }
+            c += cost_of(rows, t.units);
+            if (++g == Hkv) {
+                g = 0;
+                ++i;
+                t = next;
+                next = tiles[min(i + 1, last)];
+            }
+            if (some) return true;
+        }
+        return false;
+    }
+};
 
 // shared_attn_tc.cu: the tensor-core kernel (bf16)
 cudaError_t launch_attn_tc(const AttnArgs &a, int num_sms, cudaStream_t st);

@@ -40,21 +40,14 @@ struct Smem {
     int page[kKB];
 };
 
-struct Seg {
-    Tile t;
-    int g, k0, k1;        // KV head, keys [k0, k1)
-    bool direct;          // no other segment or tile has keys of these tokens
-    long long prow;       // first partial row
-};
-
 template <int D>
-__device__ void load_keys(const AttnArgs &a, const Seg &s, int kb, const int *list, Smem<D> &sm) {
+__device__ void load_keys(const AttnArgs &a, const Seg &s, int k1, int kb, const int *list, Smem<D> &sm) {
     constexpr int LD = Smem<D>::LD, C = D / 4;
     const int tid = threadIdx.x;
     if (tid < kKB) {
         const int key = kb + tid;
         int id = -1;
-        if (key < s.k1) {
+        if (key < k1) {
             id = list[key >> a.shift];
             if (id < 0 || id >= a.n_pages) {
                 id = -1;
@@ -83,6 +76,7 @@ __device__ void run_segment(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
     constexpr int LD = Smem<D>::LD, LP = Smem<D>::LP, BR = 16 * MR, NC = D / 64;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int rows = s.t.ntok * a.G;
+    const int k0 = s.k * kUnitKeys, k1 = min((s.k + s.n) * kUnitKeys, s.t.keys);  // keys of the segment
     const bool local = s.t.flags & kLocal;
     const int *list = local ? a.table + (size_t)s.t.owner * a.max_pages
                             : a.prefix_table + (size_t)s.t.owner * a.max_prefix_pages;
@@ -105,13 +99,13 @@ __device__ void run_segment(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
             m[i] = kNegInf;
             l[i] = 0.f;
             const int rr = rb + ty * MR + i;
-            lim[i] = min(s.k1, local ? s.t.base + rr / a.G + 1 : s.t.keys);
+            lim[i] = min(k1, local ? s.t.base + rr / a.G + 1 : s.t.keys);
 #pragma unroll
             for (int c = 0; c < 4 * NC; ++c) o[i][c] = 0.f;
         }
-        for (int kb = s.k0; kb < s.k1; kb += kKB) {
+        for (int kb = k0; kb < k1; kb += kKB) {
             __syncthreads();
-            load_keys<D>(a, s, kb, list, sm);
+            load_keys<D>(a, s, k1, kb, list, sm);
             float sc[MR][4];
 #pragma unroll
             for (int i = 0; i < MR; ++i)
@@ -164,7 +158,7 @@ __device__ void run_segment(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
                 for (int c = 0; c < 4 * NC; ++c) o[i][c] *= al;
             }
             __syncwarp();
-            const int kn = min(kKB, s.k1 - kb);
+            const int kn = min(kKB, k1 - kb);
             for (int k = 0; k < kn; k += 4) {
                 float4 px[MR];
 #pragma unroll
@@ -205,12 +199,11 @@ __device__ void run_segment(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
                 }
                 if (a.lse && tx == 0) a.lse[th] = l[i] == 0.f ? kNegInf : (m[i] + log2f(l[i])) * kLn2;
             } else {
-                const size_t row = (size_t)(s.prow + rr);
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
-                    *reinterpret_cast<float4 *>(a.ws_o + row * D + 64 * c + 4 * tx) =
+                    *reinterpret_cast<float4 *>(a.ws_o + partial_at(s.prow, rows, rr, 64 * c + 4 * tx, D)) =
                         make_float4(o[i][4 * c], o[i][4 * c + 1], o[i][4 * c + 2], o[i][4 * c + 3]);
-                if (tx == 0) a.ws_ml[row] = make_float2(m[i], l[i]);
+                if (tx == 0) a.ws_ml[s.prow + rr] = make_float2(m[i], l[i]);
             }
         }
     }
@@ -226,32 +219,11 @@ shared_attn_kernel(const AttnArgs a) {
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicExch(a.ws_err, (int)ASM_ERR_INVALID_ARG);
         return;
     }
-    for (int w = blockIdx.x; w < h.workers; w += gridDim.x) {
-        long long u = (long long)w * h.upc;
-        const long long end = min(h.W, u + h.upc);
-        if (u >= end) break;
-        int i = a.first[w];
-        while (u < end) {
-            Seg s;
-            s.t = a.tiles[i];
-            if (s.t.units == 0) {
-                ++i;
-                continue;
-            }
-            const long long t0 = s.t.unit0 * a.Hkv, rel = u - t0;
-            s.g = (int)(rel / s.t.units);
-            const int k = (int)(rel - (long long)s.g * s.t.units);
-            const int n = (int)min((long long)(s.t.units - k), end - u);
-            const long long c0 = t0 + (long long)s.g * s.t.units;
-            s.k0 = k * kUnitKeys;
-            s.k1 = min((k + n) * kUnitKeys, s.t.keys);
-            s.direct = (s.t.flags & kDirect) && n == s.t.units;
-            s.prow = partial_row(s.t, a.G, s.g, w - (int)(c0 / h.upc));
-            if (s.t.ntok * a.G <= 16) run_segment<D, 1>(a, s, sm);
-            else run_segment<D, 4>(a, s, sm);
-            u += n;
-            if (k + n == s.t.units && s.g == a.Hkv - 1) ++i;
-        }
+    Walk walk(a, h, blockIdx.x);  // one block per worker
+    Seg s;
+    while (walk.step(s)) {
+        if (s.t.ntok * a.G <= 16) run_segment<D, 1>(a, s, sm);
+        else run_segment<D, 4>(a, s, sm);
     }
 }
 
@@ -281,18 +253,19 @@ shared_merge_kernel(const AttnArgs a) {
         const int2 tt = live ? a.tok[t] : make_int2(-1, -1);
         live = live && tt.x >= 0;  // tokens outside every row are left as they are
         const int g = hq / a.G, hh = hq - g * a.G;
-        long long row[2] = {0, 0}, step[2] = {0, 0};
-        int n[2] = {0, 0};
+        long long row[2] = {0, 0};            // first partial row of the pair's segments
+        int rows[2] = {0, 0}, at[2] = {0, 0}, n[2] = {0, 0};
         if (live) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int i = x == 0 ? tt.x : tt.y;
                 if (i < 0) continue;
                 const Tile tl = a.tiles[i];
-                n[x] = segments((tl.unit0 * a.Hkv) + (long long)g * tl.units, tl.units, h.upc);
+                rows[x] = tl.ntok * a.G;
+                n[x] = segments(tl.cost0 * a.Hkv + g * cost_of(rows[x], tl.units), rows[x], tl.units, h.range);
                 if (x == 0 && n[x] == 1 && (tl.flags & kDirect)) live = false;  // already written
-                step[x] = (long long)tl.ntok * a.G;
-                row[x] = partial_row(tl, a.G, g, 0) + (long long)(t - tl.tok0) * a.G + hh;
+                row[x] = tl.row0 + (long long)g * tl.cap * rows[x];
+                at[x] = (t - tl.tok0) * a.G + hh;
             }
         }
         const int tot = live ? n[0] + n[1] : 0;
@@ -301,7 +274,8 @@ shared_merge_kernel(const AttnArgs a) {
         for (int e = 0; e < E; ++e) o[e] = 0.f;
         for (int e0 = sub * 32; e0 < tot; e0 += NW * 32) {
             const int e = e0 + lane;
-            const long long r = e < n[0] ? row[0] + e * step[0] : row[1] + (e - n[0]) * step[1];
+            const long long r = e < n[0] ? row[0] + (long long)e * rows[0] + at[0]
+                                         : row[1] + (long long)(e - n[0]) * rows[1] + at[1];
             const float2 ml = e < tot ? __ldcg(a.ws_ml + r) : make_float2(kNegInf, 0.f);
             const float mn = fmaxf(m, warp_max(ml.x)), ref = mn == kNegInf ? 0.f : mn;
             const float al = exp2f(m - ref), w = ml.y == 0.f ? 0.f : exp2f(ml.x - ref);
@@ -315,8 +289,9 @@ shared_merge_kernel(const AttnArgs a) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int ee = e0 + min(j0 + j, cnt - 1);
-                    const long long rr = ee < n[0] ? row[0] + ee * step[0] : row[1] + (ee - n[0]) * step[1];
-                    const float *p = a.ws_o + rr * D + lane * E;
+                    const float *p = a.ws_o + (ee < n[0] ? partial_at(row[0] + (long long)ee * rows[0], rows[0], at[0], lane * E, D)
+                                                         : partial_at(row[1] + (long long)(ee - n[0]) * rows[1], rows[1], at[1],
+                                                                      lane * E, D));
 #pragma unroll
                     for (int d = 0; d < E; ++d) v[j][d] = __ldcg(p + d);
                 }

@@ -1,35 +1,37 @@
 // shared_attn_tc.cu -- attention of a ragged batch over shared prefixes and
 // the rows' own pages on the tensor cores (bf16 storage).
 //
-// One CTA per SM takes one worker's range of the plan's units (128 keys of
-// one tile for one KV head) and works segment by segment: S = Q K^T and
-// O += P V on tcgen05.mma, fp32 accumulators in tensor memory, the softmax in
-// registers with a running maximum that is only raised when it grows by more
-// than 8 (base 2; numerator and denominator share it, so a stale maximum is
-// exact).  Warp roles:
-//   warp 0     producer: the page ids of a unit (one lane per page, read one
-//              unit ahead), then one TMA box per page and 64 columns, K and V
-//              tiles in turn through a ring that runs on across segments;
-//   warp 1     tensor memory; one lane issues the products;
-//   warps 2-5  softmax stream 0, warps 6-9 softmax stream 1: a thread per
+// One CTA per SM takes one worker's range of the plan's line and works segment
+// by segment: S = Q K^T and O += P V on tcgen05.mma, fp32 accumulators in
+// tensor memory, the softmax in registers with a running maximum that is only
+// raised when it grows by more than 8 (base 2; numerator and denominator share
+// it, so a stale maximum is exact).  Warp roles:
+//   warp 8     producer: a segment's queries (TMA over [T][Hkv][G][d]), then
+//              the page ids of a unit (one lane per page, read one unit ahead)
+//              and one TMA box per page and 64 columns, K and V tiles in turn
+//              through a ring that runs on across segments;
+//   warp 9     tensor memory; one lane issues the products;
+//   warps 0-3  softmax stream 0, warps 4-7 softmax stream 1: a thread per
 //              query row (tensor-memory lane).  In units that end a tile's
 //              keys they also clear the places of V behind the last key, and
 //              the non-finite values of keys that some of the tile's rows do
 //              not see (0 times a NaN would reach those rows); the epilogue
 //              adds them back to the rows that do.
-// A tile of more than 128 rows gives each stream 128 of its rows and all keys
-// (one read of K and V serves 256 rows); a smaller one gives both streams the
-// same rows and every other unit of keys, so that in either case one stream's
-// softmax runs under the other's products.  The two states of a row are
-// joined in the epilogue.  Decode tiles with a few rows waste most of a
-// product, which costs nothing: a 128-key unit takes the tensor core 0.8 us
-// at most and 64 KB take an SM's share of HBM 1.5 us; warps without rows skip
-// the softmax.
+// The work is a sequence of steps that alternate between the streams, across
+// segments too.  A tile of more than 128 rows gives each stream 128 of its
+// rows, so a unit is two steps (one read of K and V serves 256 rows); in a
+// smaller one a unit is one step, and a segment of two or more units leaves a
+// state in both streams, which its epilogue joins.  The scores of step i + 2
+// are issued right behind the P V of step i, so one stream's softmax and
+// epilogue run under the other's products.
+// Decode tiles with a few rows waste most of a product, which costs nothing:
+// a 128-key unit takes the tensor core 0.6 us and 64 KB take an SM's share of
+// HBM 1.5 us; warps without rows skip the softmax.
 // Tensor memory columns: O_0 [0,128) O_1 [128,256) S_0 / P_0 [256,384)
 // S_1 / P_1 [384,512).  Products complete in issue order, so S_x(next) (issued
 // after P_x V) overwrites P_x only once it was read, and its completion means
-// that O_x is stable.  Every wait is bounded; a timeout ends the CTA's waits and
-// sets the error word.
+// that O_x is stable.  Every wait is bounded; after a timeout a warp waits no
+// more, keeps to the barriers it shares with others, and the error word is set.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -48,11 +50,13 @@ namespace tc {
 using namespace umma;
 
 constexpr int kThreads = 320;
+constexpr int kProducer = 8, kIssuer = 9;
 constexpr int kSoftmax = 256;       // threads of the two softmax streams
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.f;
 constexpr int kBox = 128 * 128;     // 128 rows x 64 columns of bf16
 constexpr int kFixUnits = 4;        // units of a tile that some of its rows see in part
+constexpr int kSmallRows = 32;      // query rows of the small box
 
 template <int D>
 struct Cfg {
@@ -66,14 +70,14 @@ struct Smem {
     unsigned char q[2][Cfg<D>::TILE];
     unsigned char kv[Cfg<D>::RING][Cfg<D>::TILE];
     float2 ml[2][128];                 // a row's (max, sum) in each stream
-    uint32_t fix[kFixUnits][4];        // keys whose V was cleared, from the first masked unit on
+    uint32_t fix[4][kFixUnits][4];     // per segment (modulo 4): keys whose V was cleared, from the first masked unit on
     uint64_t kv_full[Cfg<D>::RING], kv_empty[Cfg<D>::RING];
-    uint64_t q_full, s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
     uint32_t tmem_base;
 };
 
 struct Maps {
-    CUtensorMap k, v;
+    CUtensorMap k, v, q, q_small;
 };
 
 __device__ __forceinline__ void set_error(int *err, asm_status s) { atomicExch(err, (int)s); }
@@ -105,59 +109,12 @@ __device__ __forceinline__ uint64_t exp2_poly_x2(uint64_t t2) {
     return pack_u32x2((uint32_t)p + ((uint32_t)y << 23), (uint32_t)(p >> 32) + ((uint32_t)(y >> 32) << 23));
 }
 
-// Barrier of the softmax warps; true if any of their threads passes true.
-__device__ __forceinline__ bool softmax_any(bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, %2, p;\n"
-        " selp.u32 %0, 1, 0, q;\n}\n"
-        : "=r"(r) : "r"((uint32_t)v), "n"(kSoftmax) : "memory");
-    return r != 0;
+// Barrier of the softmax warps: both streams, or one.
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftmax) : "memory"); }
+__device__ __forceinline__ void stream_sync(int x) {
+    if (x == 0) asm volatile("bar.sync 2, 128;" ::: "memory");
+    else asm volatile("bar.sync 3, 128;" ::: "memory");
 }
-
-// The segments of one worker, in order.  Every role walks them by itself; the
-// next tile's descriptor is read ahead.
-struct Seg {
-    Tile t;
-    int g, k, n;          // KV head, first unit, units
-    bool direct;          // no other segment or tile has keys of these tokens
-    long long prow;       // first partial row
-};
-struct Walk {
-    const AttnArgs &a;
-    const Header &h;
-    long long u, end;
-    int w, i;
-    Tile t, next;
-    __device__ Walk(const AttnArgs &a_, const Header &h_, int w_) : a(a_), h(h_), w(w_) {
-        u = (long long)w * h.upc;
-        end = min(h.W, u + h.upc);
-        i = 0;
-        if (u < end) {
-            i = a.first[w];
-            t = a.tiles[i];
-            next = a.tiles[min(i + 1, h.ntiles - 1)];
-        }
-    }
-    __device__ bool step(Seg &s) {
-        if (u >= end) return false;
-        while (u >= t.unit0 * a.Hkv + (long long)t.units * a.Hkv) {
-            ++i;
-            t = next;
-            next = a.tiles[min(i + 1, h.ntiles - 1)];
-        }
-        const long long t0 = t.unit0 * a.Hkv;
-        s.t = t;
-        s.g = (int)((u - t0) / t.units);
-        const long long c0 = t0 + (long long)s.g * t.units;
-        s.k = (int)(u - c0);
-        s.n = (int)min((long long)(t.units - s.k), end - u);
-        s.direct = (t.flags & kDirect) && s.n == t.units;
-        s.prow = partial_row(t, a.G, s.g, w - (int)(c0 / h.upc));
-        u += s.n;
-        return true;
-    }
-};
 
 // First unit (of the tile) that holds a key some row of the tile does not
 // see, when keys end at the row's own token; the tile's units if there is none.
@@ -210,15 +167,17 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
             mbar_init(&sm.kv_full[i], 1);
             mbar_init(&sm.kv_empty[i], 1);
         }
-        mbar_init(&sm.q_full, kSoftmax);
         for (int x = 0; x < 2; ++x) {
+            mbar_init(&sm.q_full[x], 1);
+            mbar_init(&sm.q_empty[x], 1);
             mbar_init(&sm.s_full[x], 1);
             mbar_init(&sm.p_full[x], 128);
             mbar_init(&sm.o_full[x], 1);
         }
         fence_mbar_init();
     }
-    if (warp == 1) {
+    if (tid < 4 * kFixUnits * 4) (&sm.fix[0][0][0])[tid] = 0;
+    if (warp == kIssuer) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(smem_addr(&sm.tmem_base)), "r"(kTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -233,20 +192,39 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
     const Header h = *a.hdr;
     const bool fits = plan_ok(a, h);
     if (!fits && blockIdx.x == 0 && tid == 0) set_error(a.ws_err, ASM_ERR_INVALID_ARG);
-    const int w = blockIdx.x;
     bool ok = true;
     // the lanes of a warp agree on a timeout, so that none leaves the others in a collective
     auto wait = [&](uint64_t *bar, uint32_t parity) { ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity)); };
 
-    if (!fits || w >= h.workers) {
-        // nothing to do for this CTA
-    } else if (warp == 0) {
+    if (!fits) {
+        // nothing to do
+    } else if (warp == kProducer) {
         // ------------------------------------------------------ producer
         const int rows = min(a.S, kUnitKeys), boxes = kUnitKeys / rows;  // keys and boxes per page of a unit
-        Walk walk(a, h, w);
+        const int tok_x = kTileRows / a.G;                               // tokens of 128 query rows
+        Walk walk(a, h, blockIdx.x);
         Seg s;
         uint32_t n = 0;            // ring items so far
-        while (walk.step(s)) {
+        uint32_t qn[2] = {0, 0};   // fills of the query buffers
+        int qb = 0;                // buffer of the next small tile
+        while (ok && walk.step(s)) {
+            const int qrows = s.t.ntok * a.G;
+            const bool dual = qrows > kTileRows, small = qrows <= kSmallRows;
+            for (int x = 0; x < 2; ++x) {
+                if (!dual && x != qb) continue;
+                if (qn[x] > 0) wait(&sm.q_empty[x], (qn[x] - 1) & 1);
+                if (!ok) break;
+                ++qn[x];
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sm.q_full[x], C::HALVES * 128 * (small ? kSmallRows : kTileRows));
+#pragma unroll
+                    for (int hf = 0; hf < C::HALVES; ++hf)
+                        tma_load_4d(sm.q[x] + hf * kBox, small ? &maps.q_small : &maps.q, 64 * hf, 0, s.g,
+                                    s.t.tok0 + (dual ? x * tok_x : 0), &sm.q_full[x]);
+                }
+                __syncwarp();
+            }
+            if (!dual) qb ^= 1;
             const int *list = (s.t.flags & kLocal) ? a.table + (size_t)s.t.owner * a.max_pages
                                                    : a.prefix_table + (size_t)s.t.owner * a.max_prefix_pages;
             auto page = [&](int unit) {     // this lane's page of a unit
@@ -254,7 +232,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 return (lane < boxes && unit < s.k + s.n && key < s.t.keys) ? list[key >> a.shift] : -1;
             };
             int ahead = page(s.k);
-            for (int j = s.k; j < s.k + s.n; ++j) {
+            for (int j = s.k; j < s.k + s.n && ok; ++j) {
                 const int id = ahead;
                 ahead = page(j + 1);
                 const bool used = lane < boxes && j * kUnitKeys + lane * rows < s.t.keys;
@@ -262,10 +240,11 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 if (bad) set_error(a.ws_err, ASM_ERR_INVALID_ARG);
                 // past the cache (zero fill) for places behind the last key and bad ids
                 const int c2 = used && !bad ? id * a.Hkv + s.g : a.n_pages * a.Hkv;
-                for (int kv = 0; kv < 2; ++kv, ++n) {
+                for (int kv = 0; kv < 2; ++kv) {
                     const int slot = n % RING;
                     if (n >= RING) wait(&sm.kv_empty[slot], ((n / RING) - 1) & 1);
                     if (!ok) break;
+                    ++n;
                     if (lane == 0) mbar_arrive_expect_tx(&sm.kv_full[slot], C::TILE);
                     __syncwarp();
                     if (lane < boxes) {
@@ -275,215 +254,191 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                                         &sm.kv_full[slot]);
                     }
                 }
-                if (!ok) break;
             }
-            if (!ok) break;
         }
         // every copy that was issued has landed before the CTA may end
         for (uint32_t i = n > RING ? n - RING : 0; i < n; ++i)
             if (!mbar_wait(&sm.kv_full[i % RING], (i / RING) & 1)) ok = false;
-    } else if (warp == 1) {
+        for (int x = 0; x < 2; ++x)
+            if (qn[x] > 0 && !mbar_wait(&sm.q_full[x], (qn[x] - 1) & 1)) ok = false;
+    } else if (warp == kIssuer) {
         // ------------------------------------------------- MMA issuer
         const uint32_t idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kUnitKeys >> 3) << 17) |
                                  ((uint32_t)(128 >> 4) << 24);
         const uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
                                  ((uint32_t)(128 >> 4) << 24);
-        Walk walk(a, h, w);
-        Seg s;
-        uint32_t base = 0;         // ring item of the segment's first K
-        uint32_t pn[2] = {0, 0};   // P tiles taken from each stream
-        uint32_t segs = 0;
-        auto slot_of = [&](uint32_t item) { return item % RING; };
-        auto wait_kv = [&](uint32_t item) { wait(&sm.kv_full[slot_of(item)], (item / RING) & 1); };
-        while (ok && walk.step(s)) {
-            const bool dual = s.t.ntok * a.G > kTileRows;
-            const int n = s.n;
-            auto issue_s = [&](int x, uint32_t item) {
-                if (lane == 0) {
-                    const uint32_t qb = smem_addr(sm.q[dual ? x : 0]), kb = smem_addr(sm.kv[slot_of(item)]);
+        // Two cursors over the steps: the scores run two steps ahead of the
+        // outputs.  Step i belongs to stream i & 1.  A segment is kept as
+        // 2 units + (256-row tile); the outputs' cursor takes those that the
+        // scores' cursor has entered from a queue (two steps: two at most).
+        Walk walk(a, h, blockIdx.x);
+        auto fetch = [&]() {
+            Seg s;
+            return walk.step(s) ? 2 * s.n + (s.t.ntok * a.G > kTileRows ? 1 : 0) : 0;
+        };
+        int s_seg = fetch(), p_seg = s_seg, q0 = 0, q1 = 0;
+        uint32_t s_step = 0, s_unit = 0, p_step = 0, p_unit = 0;   // steps and units before the cursor
+        int s_j = 0, s_half = 0, p_j = 0, p_half = 0;              // unit of the segment, step of a 256-row unit
+        uint32_t q_bits = 0;       // phases of the query buffers
+        int qb = 0;                // buffer of the next small tile
+        auto issue_s = [&]() {
+            const bool dual = s_seg & 1;
+            const int x = s_step & 1, b = dual ? x : qb;
+            // the first step on a query buffer waits for it, the last frees it
+            if (s_j == 0) {
+                wait(&sm.q_full[b], (q_bits >> b) & 1);
+                q_bits ^= 1u << b;
+            }
+            const uint32_t slot = (2 * s_unit) % RING;
+            if (s_half == 0) wait(&sm.kv_full[slot], ((2 * s_unit) / RING) & 1);
+            if (!ok) return;
+            tc_fence_after();
+            const bool last = s_j == (s_seg >> 1) - 1, done = !dual || s_half == 1;
+            if (lane == 0) {
+                const uint32_t qa = smem_addr(sm.q[b]), ka = smem_addr(sm.kv[slot]);
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (uint32_t)((kk >> 2) * kBox + (kk & 3) * 32);
-                        umma_bf16(tmem + 256 + (uint32_t)(x * 128), desc_k_sw128(qb + off), desc_k_sw128(kb + off),
-                                  idesc_s, kk > 0 ? 1u : 0u);
-                    }
-                    umma_commit(&sm.s_full[x]);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (uint32_t)((kk >> 2) * kBox + (kk & 3) * 32);
+                    umma_bf16(tmem + 256 + (uint32_t)(x * 128), desc_k_sw128(qa + off), desc_k_sw128(ka + off), idesc_s,
+                              kk > 0 ? 1u : 0u);
                 }
-            };
-            auto issue_pv = [&](int x, uint32_t item, bool first) {
-                if (lane == 0) {
-                    const uint32_t vb = smem_addr(sm.kv[slot_of(item)]);
+                umma_commit(&sm.s_full[x]);
+                if (done) umma_commit(&sm.kv_empty[slot]);
+                if (last) umma_commit(&sm.q_empty[b]);
+            }
+            __syncwarp();
+            ++s_step;
+            if (!done) {
+                s_half = 1;
+                return;
+            }
+            s_half = 0;
+            ++s_unit;
+            ++s_j;
+            if (last) {
+                if (!dual) qb ^= 1;
+                s_j = 0;
+                s_seg = fetch();
+                if (q0 == 0) q0 = s_seg;
+                else q1 = s_seg;
+            }
+        };
+        for (int i = 0; i < 2 && ok && s_seg != 0; ++i) issue_s();
+        uint32_t p_bits = 0;       // phases of the streams' P tiles
+        while (ok && p_seg != 0) {
+            const bool dual = p_seg & 1;
+            const int x = p_step & 1, n = p_seg >> 1;
+            const uint32_t item = 2 * p_unit + 1, slot = item % RING;
+            if (p_half == 0) wait(&sm.kv_full[slot], (item / RING) & 1);
+            wait(&sm.p_full[x], (p_bits >> x) & 1);
+            p_bits ^= 1u << x;
+            if (!ok) break;
+            tc_fence_after();
+            const bool done = !dual || p_half == 1;
+            if (lane == 0) {
+                const uint32_t va = smem_addr(sm.kv[slot]);
+                const bool fresh = dual ? p_j == 0 : p_j < 2;   // the stream's first step of the segment
 #pragma unroll
-                    for (int kk = 0; kk < kUnitKeys / 16; ++kk)
-                        umma_bf16_ts(tmem + (uint32_t)(x * 128), tmem + 256 + (uint32_t)(x * 128 + kk * 8),
-                                     desc_mn_sw128(vb + (uint32_t)(kk * 2048), kBox), idesc_o,
-                                     (!first || kk > 0) ? 1u : 0u);
-                }
-            };
-            auto commit = [&](uint64_t *bar) {
-                if (lane == 0) umma_commit(bar);
-            };
-            auto item_k = [&](int j) { return base + 2 * (uint32_t)j; };
-            auto item_v = [&](int j) { return base + 2 * (uint32_t)j + 1; };
-
-            wait(&sm.q_full, segs & 1);
-            if (dual) {
-                wait_kv(item_k(0));
-                tc_fence_after();
-                issue_s(0, item_k(0));
-                issue_s(1, item_k(0));
-                commit(&sm.kv_empty[slot_of(item_k(0))]);
-                for (int j = 0; j < n && ok; ++j) {
-                    const bool more = j + 1 < n;
-                    wait_kv(item_v(j));
-                    for (int x = 0; x < 2; ++x) {
-                        wait(&sm.p_full[x], pn[x] & 1);
-                        ++pn[x];
-                        tc_fence_after();
-                        issue_pv(x, item_v(j), j == 0);
-                        if (more) {
-                            if (x == 0) wait_kv(item_k(j + 1));
-                            issue_s(x, item_k(j + 1));
-                        } else {
-                            commit(&sm.o_full[x]);
-                        }
-                    }
-                    commit(&sm.kv_empty[slot_of(item_v(j))]);
-                    if (more) commit(&sm.kv_empty[slot_of(item_k(j + 1))]);
-                }
-            } else {
-                for (int j = 0; j < min(n, 2); ++j) {
-                    wait_kv(item_k(j));
-                    tc_fence_after();
-                    issue_s(j, item_k(j));
-                    commit(&sm.kv_empty[slot_of(item_k(j))]);
-                }
-                for (int j = 0; j < n && ok; ++j) {
-                    const int x = j & 1;
-                    wait_kv(item_v(j));
-                    wait(&sm.p_full[x], pn[x] & 1);
-                    ++pn[x];
-                    tc_fence_after();
-                    issue_pv(x, item_v(j), j < 2);
-                    commit(&sm.kv_empty[slot_of(item_v(j))]);
-                    if (j + 2 < n) {
-                        wait_kv(item_k(j + 2));
-                        issue_s(x, item_k(j + 2));
-                        commit(&sm.kv_empty[slot_of(item_k(j + 2))]);
-                    } else {
-                        commit(&sm.o_full[x]);
-                    }
+                for (int kk = 0; kk < kUnitKeys / 16; ++kk)
+                    // 16 keys a step: 8 tensor-memory columns of P, 16 rows of V
+                    umma_bf16_ts(tmem + (uint32_t)(x * 128), tmem + 256 + (uint32_t)(x * 128 + kk * 8),
+                                 desc_mn_sw128(va + (uint32_t)(kk * 2048), kBox), idesc_o, (!fresh || kk > 0) ? 1u : 0u);
+                if (dual ? p_j == n - 1 : p_j >= n - 2) umma_commit(&sm.o_full[x]);
+                if (done) umma_commit(&sm.kv_empty[slot]);
+            }
+            __syncwarp();
+            ++p_step;
+            p_half = done ? 0 : 1;
+            if (done) {
+                ++p_unit;
+                if (++p_j == n) {
+                    p_j = 0;
+                    p_seg = q0;
+                    q0 = q1;
+                    q1 = 0;
                 }
             }
-            base += 2 * (uint32_t)n;
-            ++segs;
+            if (s_seg != 0) issue_s();
         }
-        __syncwarp();
     } else {
         // ----------------------------------------------------- softmax
-        const int x = (warp - 2) >> 2;      // stream
+        const int x = warp >> 2;            // stream
         const int qd = warp & 3;            // tensor-memory lane quarter
         const int row = qd * 32 + lane;     // row within the stream's 128
-        const int st = tid - 64;            // thread among the softmax threads
         const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
         const uint32_t t_s = tmem + lane_off + 256 + (uint32_t)(x * 128);
         const float sl2 = a.sl2;
-        Walk walk(a, h, w);
+        Walk walk(a, h, blockIdx.x);
         Seg s;
-        uint32_t sn = 0, on[2] = {0, 0}, base = 0;   // base: ring item of the segment's first K
-        while (walk.step(s)) {
+        uint32_t sn = 0, on[2] = {0, 0};    // scores taken, outputs finished in each stream
+        uint32_t step = 0, unit0 = 0, seg = 0;   // steps, units and segments before this segment
+        for (; walk.step(s); ++seg, unit0 += (uint32_t)s.n) {
             const int rows = s.t.ntok * a.G;
             const bool dual = rows > kTileRows, local = s.t.flags & kLocal;
-            // ---- the tile's queries into the swizzled operand layout
-            {
-                const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) +
-                                         ((size_t)s.t.tok0 * a.Hq + (size_t)s.g * a.G) * D;
-                constexpr int CH = D / 8;
-#pragma unroll 4
-                for (int i = st; i < rows * CH; i += kSoftmax) {
-                    const int r = i / CH, c = i - r * CH, tk = r / a.G, hh = r - tk * a.G;
-                    const uint4 v = *reinterpret_cast<const uint4 *>(q + ((size_t)tk * a.Hq + hh) * D + c * 8);
-                    *reinterpret_cast<uint4 *>(sm.q[r >> 7] + (c >> 3) * kBox + swz128(r & 127, c & 7)) = v;
-                }
-                if (st < kFixUnits * 4) sm.fix[st >> 2][st & 3] = 0;
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                mbar_arrive(&sm.q_full);
+            const int j0 = dual ? 0 : (x ^ (int)(step & 1)), dj = dual ? 1 : 2;   // this stream's units
+            step += (uint32_t)(dual ? 2 * s.n : s.n);
+            if (j0 >= s.n) {                 // a single unit, on the other stream
+                ++on[x ^ 1];
+                continue;
             }
-            const int first = dual ? 0 : x, step = dual ? 1 : 2;
+            const bool joint = dual || s.n > 1;             // both streams have steps
             const int r = dual ? x * 128 + row : row;       // row of the tile
             const bool live = r < rows;
             const bool warp_live = (dual ? x * 128 : 0) + qd * 32 < rows;
             const int tk = r / a.G;
             const int masked = first_masked_unit(s.t);
-            const int lim = live ? (local ? min(s.t.base + tk + 1, s.t.keys) : s.t.keys) : s.t.keys;
+            const int lim = live && local ? min(s.t.base + tk + 1, s.t.keys) : s.t.keys;
+            uint32_t(&fix)[kFixUnits][4] = sm.fix[seg & 3];
             float m_used = kNegInf, l = 0.f;
-            int j = first;
-            for (; j < s.n; j += step) {
+            for (int j = j0; j < s.n; j += dj) {
                 wait(&sm.s_full[x], sn & 1);
                 ++sn;
-                if (!ok) break;
                 tc_fence_after();
                 if (warp_live) {
                     const int vis = lim - (s.k + j) * kUnitKeys;   // keys of this unit the row sees
                     const bool part = __any_sync(0xffffffffu, vis < kUnitKeys);
-                    float mraw = kNegInf;
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32];
-                        tmem_ld32(t_s + (uint32_t)(32 * c), v);
-                        tmem_wait_ld();
-                        if (part) {
+                    uint32_t v[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(t_s + (uint32_t)(32 * c), v[c]);
+                    tmem_wait_ld();
+                    if (part) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (32 * c + i >= vis) v[i] = 0xff800000u;  // -inf
-                        }
+                                if (32 * c + i >= vis) v[c][i] = 0xff800000u;  // -inf
+                    }
+                    float mc[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
                         float m11[11];
 #pragma unroll
                         for (int i = 0; i < 10; ++i)
-                            m11[i] = max3_nan(__uint_as_float(v[3 * i]), __uint_as_float(v[3 * i + 1]),
-                                              __uint_as_float(v[3 * i + 2]));
-                        m11[10] = max_nan(__uint_as_float(v[30]), __uint_as_float(v[31]));
-                        mraw = max3_nan(mraw, max3_nan(max3_nan(m11[0], m11[1], m11[2]), max3_nan(m11[3], m11[4], m11[5]),
-                                                       max3_nan(m11[6], m11[7], m11[8])), max_nan(m11[9], m11[10]));
+                            m11[i] = max3_nan(__uint_as_float(v[c][3 * i]), __uint_as_float(v[c][3 * i + 1]),
+                                              __uint_as_float(v[c][3 * i + 2]));
+                        m11[10] = max_nan(__uint_as_float(v[c][30]), __uint_as_float(v[c][31]));
+                        mc[c] = max3_nan(max3_nan(max3_nan(m11[0], m11[1], m11[2]), max3_nan(m11[3], m11[4], m11[5]),
+                                                  max3_nan(m11[6], m11[7], m11[8])), m11[9], m11[10]);
                     }
-                    const float mt = mraw * sl2;
+                    const float mt = max_nan(max3_nan(mc[0], mc[1], mc[2]), mc[3]) * sl2;
                     float alpha = 1.f;
                     if (live && !(mt <= m_used + kRescale)) {   // a NaN passes, and stays
                         alpha = ex2f(m_used - mt);
                         m_used = mt;
                         l *= alpha;
                     }
-                    // tensor-memory access is warp-wide: rows that keep their maximum scale by 1
-                    if (j > first && __any_sync(0xffffffffu, alpha != 1.f)) {
-                        const uint32_t t_o = tmem + lane_off + (uint32_t)(x * 128);
-#pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(t_o + (uint32_t)c0, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                            tmem_st32(t_o + (uint32_t)c0, o);
-                        }
-                    }
                     // p = 2^(s scale log2(e) - m), rounded to bf16 for the product with V
-                    // (the sum keeps fp32); P goes over columns of S already read
+                    // (the sum keeps fp32); P goes over the columns of S
                     const float ref = m_used == kNegInf ? 0.f : m_used;
                     const uint64_t sl2x2 = pack_f32x2(sl2, sl2), negm2 = pack_f32x2(-ref, -ref);
                     uint64_t acc[4] = {0, 0, 0, 0};
-#pragma unroll 1
+#pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32];
-                        tmem_ld32(t_s + (uint32_t)(32 * c), v);
-                        tmem_wait_ld();
                         uint32_t pk[16];
                         if (part) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (32 * c + i >= vis) v[i] = 0xff800000u;
-#pragma unroll
                             for (int i = 0; i < 16; ++i) {
-                                const uint64_t t2 = fma_f32x2(pack_u32x2(v[2 * i], v[2 * i + 1]), sl2x2, negm2);
+                                const uint64_t t2 = fma_f32x2(pack_u32x2(v[c][2 * i], v[c][2 * i + 1]), sl2x2, negm2);
                                 const uint64_t p2 = pack_f32x2(ex2f(lo_f32(t2)), ex2f(hi_f32(t2)));
                                 acc[i & 3] = add_f32x2(acc[i & 3], p2);
                                 pk[i] = pack_bf16(lo_f32(p2), hi_f32(p2));
@@ -491,7 +446,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                         } else {
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
-                                const uint64_t t2 = fma_f32x2(pack_u32x2(v[2 * i], v[2 * i + 1]), sl2x2, negm2);
+                                const uint64_t t2 = fma_f32x2(pack_u32x2(v[c][2 * i], v[c][2 * i + 1]), sl2x2, negm2);
                                 uint64_t p2;
                                 if ((i & 3) == 3) p2 = exp2_poly_x2(t2);
                                 else p2 = pack_f32x2(ex2f(lo_f32(t2)), ex2f(hi_f32(t2)));
@@ -503,97 +458,108 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                     }
                     const uint64_t a01 = add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3]));
                     l += lo_f32(a01) + hi_f32(a01);
+                    // tensor-memory access is warp-wide: rows that keep their maximum scale by 1
+                    if (j > j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                        const uint32_t t_o = tmem + lane_off + (uint32_t)(x * 128);
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(t_o + (uint32_t)c0, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            tmem_st32(t_o + (uint32_t)c0, o);
+                        }
+                    }
                     tmem_wait_st();
                 }
                 const int unit = s.k + j, valid = s.t.keys - unit * kUnitKeys;
                 if (unit >= masked || valid < kUnitKeys) {
                     // V as the product may use it (both streams of a tall tile do the same)
-                    const uint32_t item = base + 2 * (uint32_t)j + 1;
+                    const uint32_t item = 2 * (unit0 + (uint32_t)j) + 1;
                     wait(&sm.kv_full[item % RING], (item / RING) & 1);
                     if (ok) {
-                        unsigned char *v = sm.kv[item % RING];
+                        unsigned char *vt = sm.kv[item % RING];
                         const int r0 = unit >= masked ? max(s.t.base + 1 - unit * kUnitKeys, 0) : kUnitKeys;
-                        clean_values<D>(v, r0, min(valid, kUnitKeys), row, sm.fix[min(max(unit - masked, 0), kFixUnits - 1)]);
+                        clean_values<D>(vt, r0, min(valid, kUnitKeys), row, fix[min(max(unit - masked, 0), kFixUnits - 1)]);
                     }
                 }
                 tc_fence_before();
                 mbar_arrive(&sm.p_full[x]);
             }
             // ------------------------------------------------------ epilogue
-            // the streams that had units (a small tile of one unit has only the first)
-            const bool two = dual || s.n > 1;
-            if (!dual) {
+            const bool fixable = masked < s.k + s.n;
+            if (joint) {
                 sm.ml[x][row] = make_float2(m_used, l);
                 wait(&sm.o_full[0], on[0] & 1);
-                ++on[0];
-                if (two) {
-                    wait(&sm.o_full[1], on[1] & 1);
-                    ++on[1];
-                }
-            } else {
-                wait(&sm.o_full[x], on[x] & 1);
+                wait(&sm.o_full[1], on[1] & 1);
                 ++on[0];
                 ++on[1];
+                softmax_sync();
+            } else {
+                wait(&sm.o_full[x], on[x] & 1);
+                ++on[x];
+                if (fixable) stream_sync(x);
             }
-            ok = !softmax_any(!ok);   // all eight warps go on or none
             tc_fence_after();
-            if (!ok) break;
+            uint32_t fixed = 0;
+            if (fixable) {
+                for (int fu = 0; fu < kFixUnits; ++fu) {
+                    const uint4 f = *reinterpret_cast<const uint4 *>(fix[fu]);
+                    fixed |= f.x | f.y | f.z | f.w;
+                }
+            }
             if (warp_live) {
+                // the states of a small tile's streams, joined
                 float w0 = 1.f, w1 = 0.f, m = m_used;
-                if (!dual) {
+                const bool two = joint && !dual;
+                if (two) {
                     const float2 s0 = sm.ml[0][row], s1 = sm.ml[1][row];
-                    m = two ? max_nan(s0.x, s1.x) : s0.x;
+                    m = max_nan(s0.x, s1.x);
                     const float ref = m == kNegInf ? 0.f : m;
                     w0 = ex2f(s0.x - ref);
-                    w1 = two ? ex2f(s1.x - ref) : 0.f;
-                    l = two ? w0 * s0.y + w1 * s1.y : w0 * s0.y;
+                    w1 = ex2f(s1.x - ref);
+                    l = w0 * s0.y + w1 * s1.y;
                 }
                 const size_t th = (size_t)(s.t.tok0 + tk) * a.Hq + (size_t)s.g * a.G + (r - tk * a.G);
                 const float inv = s.direct ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-                // a small tile's streams each write half of the columns
-                const int c_lo = dual ? 0 : x * (D / 2), c_hi = dual ? D : c_lo + D / 2;
-                const uint32_t t_o = tmem + lane_off + (dual ? (uint32_t)(x * 128) : 0u);
+                // of two streams, each writes half of the columns
+                const int c_lo = two ? x * (D / 2) : 0, c_hi = two ? c_lo + D / 2 : D;
+                const uint32_t t_o = tmem + lane_off + (two ? 0u : (uint32_t)(x * 128));
 #pragma unroll 1
                 for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
                     uint32_t o[32];
                     tmem_ld32(t_o + (uint32_t)c0, o);
-                    tmem_wait_ld();
-                    if (!dual) {
+                    if (two) {
+                        uint32_t o1[32];
+                        tmem_ld32(t_o + 128u + (uint32_t)c0, o1);
+                        tmem_wait_ld();
                         // a stream that saw no key of the row holds no value for it
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = w0 == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * w0);
-                        if (two) {
-                            uint32_t o1[32];
-                            tmem_ld32(t_o + 128u + (uint32_t)c0, o1);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (w1 != 0.f)
-                                    o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), w1, __uint_as_float(o[i])));
+                        for (int i = 0; i < 32; ++i) {
+                            const float u0 = w0 == 0.f ? 0.f : __uint_as_float(o[i]) * w0;
+                            o[i] = __float_as_uint(w1 == 0.f ? u0 : fmaf(__uint_as_float(o1[i]), w1, u0));
                         }
+                    } else {
+                        tmem_wait_ld();
                     }
-                    if (masked < s.k + s.n && live) {
+                    if (fixed && live) {
                         // non-finite values of keys that only some rows see: back into the rows that do
-                        for (int fu = 0; fu < kFixUnits; ++fu) {
-                            for (int b = 0; b < 4; ++b) {
-                                uint32_t bits = sm.fix[fu][b];
-                                while (bits) {
-                                    const int key = (masked + fu) * kUnitKeys + 32 * b + __ffs(bits) - 1;
-                                    bits &= bits - 1;
-                                    if (key >= lim) continue;
-                                    const int id = a.table[(size_t)s.t.owner * a.max_pages + (key >> a.shift)];
-                                    if (id < 0 || id >= a.n_pages) continue;
-                                    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v_pages) +
-                                        ((((long long)id * a.Hkv + s.g) << a.shift) + (key & (a.S - 1))) * D + c0;
 #pragma unroll 1
-                                    for (int i = 0; i < 32; ++i) {
-                                        const float f = __bfloat162float(v[i]);
-                                        if (!(f - f == 0.f)) {
+                        for (int f = 0; f < kFixUnits * 4; ++f) {
+                            uint32_t bits = fix[f >> 2][f & 3];
+                            while (bits) {
+                                const int key = masked * kUnitKeys + 32 * f + __ffs(bits) - 1;
+                                bits &= bits - 1;
+                                if (key >= lim) continue;
+                                const int id = a.table[(size_t)s.t.owner * a.max_pages + (key >> a.shift)];
+                                if (id < 0 || id >= a.n_pages) continue;
+                                const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(a.v_pages) +
+                                    ((((long long)id * a.Hkv + s.g) << a.shift) + (key & (a.S - 1))) * D + c0;
 #pragma unroll
-                                            for (int e = 0; e < 32; ++e)
-                                                if (e == i) o[e] = __float_as_uint(__uint_as_float(o[e]) + f);
-                                        }
-                                    }
+                                for (int i = 0; i < 32; ++i) {
+                                    const float y = __bfloat162float(vp[i]);
+                                    if (!(y - y == 0.f)) o[i] = __float_as_uint(__uint_as_float(o[i]) + y);
                                 }
                             }
                         }
@@ -611,27 +577,31 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                                 *reinterpret_cast<uint4 *>(dst + i) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                             }
                         } else {
-                            float *dst = a.ws_o + (size_t)(s.prow + r) * D + c0;
 #pragma unroll
                             for (int i = 0; i < 32; i += 4)
-                                *reinterpret_cast<uint4 *>(dst + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                                *reinterpret_cast<uint4 *>(a.ws_o + partial_at(s.prow, rows, r, c0 + i, D)) =
+                                    make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                         }
                     }
                 }
-                if (live && (dual || x == 0)) {
+                if (live && (!two || x == 0)) {
                     if (!s.direct) a.ws_ml[s.prow + r] = make_float2(m, l);
                     else if (a.lse) a.lse[th] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
                 }
             }
             tc_fence_before();
-            asm volatile("bar.sync 1, %0;" ::"n"(kSoftmax) : "memory");
-            base += 2 * (uint32_t)s.n;
+            // the other stream's outputs and statistics have been read
+            if (joint) softmax_sync();
+            if (fixed) {
+                if (!joint) stream_sync(x);
+                if (row < kFixUnits * 4) fix[row >> 2][row & 3] = 0;
+            }
         }
     }
     if (!ok && lane == 0) set_error(a.ws_err, ASM_ERR_TIMEOUT);
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == kIssuer) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
     }
@@ -641,6 +611,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
 }  // namespace shared
 
 bool make_map_3d(CUtensorMap *m, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t rows);
+bool make_map_qrows(CUtensorMap *m, const void *q, int B, int Hkv, int G, int d, int rows);
 
 namespace shared {
 
@@ -650,7 +621,9 @@ cudaError_t launch_tc(const AttnArgs &a, int num_sms, cudaStream_t st) {
     memset(&maps, 0, sizeof(maps));
     const uint64_t heads = (uint64_t)a.n_pages * a.Hkv;
     const uint32_t box = (uint32_t)(a.S < kUnitKeys ? a.S : kUnitKeys);
-    if (!make_map_3d(&maps.k, a.k_pages, D, a.S, heads, box) || !make_map_3d(&maps.v, a.v_pages, D, a.S, heads, box))
+    if (!make_map_3d(&maps.k, a.k_pages, D, a.S, heads, box) || !make_map_3d(&maps.v, a.v_pages, D, a.S, heads, box) ||
+        !make_map_qrows(&maps.q, a.q, a.T, a.Hkv, a.G, D, kTileRows) ||
+        !make_map_qrows(&maps.q_small, a.q, a.T, a.Hkv, a.G, D, tc::kSmallRows))
         return cudaErrorInvalidValue;
     auto kern = tc::shared_attn_tc_kernel<D>;
     const size_t smem = sizeof(tc::Smem<D>) + 1024;

@@ -3,7 +3,7 @@
 //
 // One block: running maxima make the offsets monotone whatever they hold,
 // then three sums over the rows, the groups and the tiles give the tile list,
-// the units before each tile and the partial rows before each tile.  Bound by
+// the cost before each tile and the partial rows before each tile.  Bound by
 // latency; a step's layers share one plan.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -128,7 +128,7 @@ shared_plan_kernel(const PlanArgs a) {
     auto prefix_keys = [&](int g) {
         return (int)min((long long)max(a.prefix_len[g], 0), (long long)a.max_prefix_pages * a.S);
     };
-    // ---- the tiles, and the units before each (chunks of one tile a thread)
+    // ---- the tiles, and the cost before each (chunks of one tile a thread)
     long long before = 0;
     for (int c = 0; c < ntiles; c += kPlanThreads) {
         const int i = c + tid;
@@ -157,15 +157,16 @@ shared_plan_kernel(const PlanArgs a) {
             }
             t.units = (t.keys + kUnitKeys - 1) / kUnitKeys;
         }
-        const long long inc = plan_scan(t.units, warp_v, 0, tot, add);
-        t.unit0 = before + inc - t.units;
+        const long long cost = cost_of(t.ntok * G, t.units);
+        const long long inc = plan_scan(cost, warp_v, 0, tot, add);
+        t.cost0 = before + inc - cost;
         before += tot;
         if (i < ntiles) tiles[i] = t;
     }
     const long long W = before * a.Hkv;
-    long long upc = (W + a.workers - 1) / a.workers;
-    upc = upc < 1 ? 1 : upc;
-    if (upc > INT32_MAX) upc = INT32_MAX;  // a table cannot be that long
+    long long range = (W + a.workers - 1) / a.workers;
+    range = range < kCostMax ? kCostMax : range;  // a range holds the start of a unit of every pair it crosses
+    if (range > INT32_MAX) range = INT32_MAX;     // a table cannot be that long
     // ---- partial rows before each tile
     before = 0;
     for (int c = 0; c < ntiles; c += kPlanThreads) {
@@ -173,7 +174,7 @@ shared_plan_kernel(const PlanArgs a) {
         long long rows = 0;
         int cap = 0;
         if (i < ntiles && tiles[i].units > 0) {
-            cap = (int)(tiles[i].units / upc) + 2;
+            cap = (int)(cost_of(tiles[i].ntok * G, tiles[i].units) / range) + 2;
             rows = (long long)cap * a.Hkv * tiles[i].ntok * G;
         }
         const long long inc = plan_scan(rows, warp_v, 0, tot, add);
@@ -181,8 +182,8 @@ shared_plan_kernel(const PlanArgs a) {
             tiles[i].cap = cap;
             tiles[i].row0 = before + inc - rows;
             // the workers whose ranges begin in this tile
-            const long long u0 = tiles[i].unit0 * a.Hkv, u1 = u0 + (long long)tiles[i].units * a.Hkv;
-            for (long long w = (u0 + upc - 1) / upc; w * upc < u1; ++w) first[w] = i;
+            const long long c0 = tiles[i].cost0 * a.Hkv, c1 = c0 + cost_of(tiles[i].ntok * G, tiles[i].units) * a.Hkv;
+            for (long long w = (c0 + range - 1) / range; w * range < c1; ++w) first[w] = i;
         }
         before += tot;
     }
@@ -206,7 +207,7 @@ shared_plan_kernel(const PlanArgs a) {
         h.magic = kMagic;
         h.R = R; h.NG = NG; h.T = a.T; h.Hq = a.Hq; h.Hkv = a.Hkv;
         h.page_size = a.S; h.max_pages = a.max_pages; h.max_prefix_pages = a.max_prefix_pages;
-        h.workers = a.workers; h.ntiles = ntiles; h.upc = (int)upc; h.W = W;
+        h.workers = a.workers; h.ntiles = ntiles; h.range = (int)range; h.W = W;
         *hdr = h;
     }
 }

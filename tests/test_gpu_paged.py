@@ -353,6 +353,17 @@ def test_shared_attention_many_rows():
     Batch("bf16", 8, 2, 64, 16, new=[1] * 600, seq=seq, goff=[0, 100, 512], pre=[70, 33], seed=4).check()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 8), (8, 1)])
+def test_shared_attention_mixes_segments(dt, Hq, Hkv):
+    """More tiles than workers: key lists of one unit and of several, tall
+    tiles and small ones, follow one another in one worker's range."""
+    rng = random.Random(2)
+    new = [rng.choice([1, 1, 1, 2, 5, 40, 70]) for _ in range(90)]
+    seq = [n + rng.choice([0, 3, 100, 128, 200, 300, 700]) for n in new]
+    Batch(dt, Hq, Hkv, 64, 32, new=new, seq=seq, goff=[4, 30, 33, 80], pre=[400, 90, 129], seed=13).check()
+
+
 def test_shared_attention_large_logits():
     """Scores of some hundreds: the running maximum moves far, weights underflow."""
     for dt in ("bf16", "f32"):
