@@ -39,8 +39,8 @@ constexpr int kDirect = 2;  // the tile holds all keys of its tokens
 
 // Cost of a tile for one KV head: COST_HEAD for its queries and its epilogue,
 // then so much per unit.  A 256-row unit costs about twice a 128-row one (the
-// tensor cores against HBM).
-constexpr int kCostMax = 4;
+// tensor cores against HBM).  A range is at least as long as the dearest unit
+// of the plan, so that it holds the start of a unit of every pair it crosses.
 __host__ __device__ inline int cost_unit(int rows) { return rows > kTileRows ? 4 : 2; }
 __host__ __device__ inline int cost_head(int rows) { return rows > kTileRows ? 4 : 3; }
 __host__ __device__ inline long long cost_of(int rows, int units) {

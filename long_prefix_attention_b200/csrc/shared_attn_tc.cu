@@ -65,14 +65,28 @@ struct Cfg {
     static constexpr int RING = D == 128 ? 4 : 8;   // K or V tiles in flight
 };
 
+// A segment as the producer hands it to the other warps; n = 0 ends the list.
+// Sixteen places are more than the producer can be ahead of the slowest reader:
+// it enters a segment only when the ring has taken all of the one before, so
+// at most RING / 2 + 3 segments are in use at a time.
+constexpr int kSegs = 16;
+struct __align__(16) SegDesc {
+    int tok0, rows, base, keys;      // first token, query rows; as in Tile
+    int g, k, n, flags;              // KV head, first unit, units; kLocal
+    long long prow;                  // first partial row
+    int owner, masked;               // row; first unit that some of the tile's rows see in part
+    int direct, pad[3];
+};
+
 template <int D>
 struct Smem {
     unsigned char q[2][Cfg<D>::TILE];
     unsigned char kv[Cfg<D>::RING][Cfg<D>::TILE];
+    SegDesc seg[kSegs];
     float2 ml[2][128];                 // a row's (max, sum) in each stream
     uint32_t fix[4][kFixUnits][4];     // per segment (modulo 4): keys whose V was cleared, from the first masked unit on
     uint64_t kv_full[Cfg<D>::RING], kv_empty[Cfg<D>::RING];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
+    uint64_t seg_full[kSegs], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
     uint32_t tmem_base;
 };
 
@@ -167,6 +181,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
             mbar_init(&sm.kv_full[i], 1);
             mbar_init(&sm.kv_empty[i], 1);
         }
+        for (int i = 0; i < kSegs; ++i) mbar_init(&sm.seg_full[i], 1);
         for (int x = 0; x < 2; ++x) {
             mbar_init(&sm.q_full[x], 1);
             mbar_init(&sm.q_empty[x], 1);
@@ -203,11 +218,31 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
         const int rows = min(a.S, kUnitKeys), boxes = kUnitKeys / rows;  // keys and boxes per page of a unit
         const int tok_x = kTileRows / a.G;                               // tokens of 128 query rows
         Walk walk(a, h, blockIdx.x);
-        Seg s;
+        uint32_t segs = 0;
+        auto publish = [&](const Seg &s, bool some) {
+            if (lane == 0) {
+                SegDesc d{};
+                if (some) {
+                    d.tok0 = s.t.tok0; d.rows = s.t.ntok * a.G; d.base = s.t.base; d.keys = s.t.keys;
+                    d.g = s.g; d.k = s.k; d.n = s.n; d.flags = s.t.flags & kLocal;
+                    d.prow = s.prow; d.owner = s.t.owner; d.masked = first_masked_unit(s.t); d.direct = s.direct;
+                }
+                sm.seg[segs % kSegs] = d;
+                mbar_arrive(&sm.seg_full[segs % kSegs]);
+            }
+            __syncwarp();
+            ++segs;
+        };
+        Seg s, ns;                 // the list is one segment ahead of the loads
+        bool some = walk.step(ns);
+        publish(ns, some);
         uint32_t n = 0;            // ring items so far
         uint32_t qn[2] = {0, 0};   // fills of the query buffers
         int qb = 0;                // buffer of the next small tile
-        while (ok && walk.step(s)) {
+        while (ok && some) {
+            s = ns;
+            some = walk.step(ns);
+            publish(ns, some);
             const int qrows = s.t.ntok * a.G;
             const bool dual = qrows > kTileRows, small = qrows <= kSmallRows;
             for (int x = 0; x < 2; ++x) {
@@ -271,10 +306,11 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
         // outputs.  Step i belongs to stream i & 1.  A segment is kept as
         // 2 units + (256-row tile); the outputs' cursor takes those that the
         // scores' cursor has entered from a queue (two steps: two at most).
-        Walk walk(a, h, blockIdx.x);
+        uint32_t segs = 0;
         auto fetch = [&]() {
-            Seg s;
-            return walk.step(s) ? 2 * s.n + (s.t.ntok * a.G > kTileRows ? 1 : 0) : 0;
+            wait(&sm.seg_full[segs % kSegs], (segs / kSegs) & 1);
+            const SegDesc &d = sm.seg[segs++ % kSegs];
+            return ok && d.n > 0 ? 2 * d.n + (d.rows > kTileRows ? 1 : 0) : 0;
         };
         int s_seg = fetch(), p_seg = s_seg, q0 = 0, q1 = 0;
         uint32_t s_step = 0, s_unit = 0, p_step = 0, p_unit = 0;   // steps and units before the cursor
@@ -368,34 +404,39 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
         const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
         const uint32_t t_s = tmem + lane_off + 256 + (uint32_t)(x * 128);
         const float sl2 = a.sl2;
-        Walk walk(a, h, blockIdx.x);
-        Seg s;
         uint32_t sn = 0, on[2] = {0, 0};    // scores taken, outputs finished in each stream
-        uint32_t step = 0, unit0 = 0, seg = 0;   // steps, units and segments before this segment
-        for (; walk.step(s); ++seg, unit0 += (uint32_t)s.n) {
-            const int rows = s.t.ntok * a.G;
-            const bool dual = rows > kTileRows, local = s.t.flags & kLocal;
+        uint32_t step = 0, unit0 = 0;       // steps and units before this segment
+        for (uint32_t seg = 0;; ++seg) {
+            // read to its end even after a timeout: the streams meet at barriers
+            const bool got = __all_sync(0xffffffffu, mbar_wait(&sm.seg_full[seg % kSegs], (seg / kSegs) & 1));
+            const SegDesc &s = sm.seg[seg % kSegs];
+            const int n = got ? s.n : 0;
+            ok = ok && got;
+            if (n == 0) break;
+            const int rows = s.rows, k0 = s.k, keys = s.keys, masked = s.masked;
+            const bool dual = rows > kTileRows;
             const int j0 = dual ? 0 : (x ^ (int)(step & 1)), dj = dual ? 1 : 2;   // this stream's units
-            step += (uint32_t)(dual ? 2 * s.n : s.n);
-            if (j0 >= s.n) {                 // a single unit, on the other stream
+            const uint32_t item0 = 2 * unit0;
+            step += (uint32_t)(dual ? 2 * n : n);
+            unit0 += (uint32_t)n;
+            if (j0 >= n) {                   // a single unit, on the other stream
                 ++on[x ^ 1];
                 continue;
             }
-            const bool joint = dual || s.n > 1;             // both streams have steps
+            const bool joint = dual || n > 1;             // both streams have steps
             const int r = dual ? x * 128 + row : row;       // row of the tile
             const bool live = r < rows;
             const bool warp_live = (dual ? x * 128 : 0) + qd * 32 < rows;
             const int tk = r / a.G;
-            const int masked = first_masked_unit(s.t);
-            const int lim = live && local ? min(s.t.base + tk + 1, s.t.keys) : s.t.keys;
+            const int lim = live && (s.flags & kLocal) ? min(s.base + tk + 1, keys) : keys;
             uint32_t(&fix)[kFixUnits][4] = sm.fix[seg & 3];
             float m_used = kNegInf, l = 0.f;
-            for (int j = j0; j < s.n; j += dj) {
+            for (int j = j0; j < n; j += dj) {
                 wait(&sm.s_full[x], sn & 1);
                 ++sn;
                 tc_fence_after();
                 if (warp_live) {
-                    const int vis = lim - (s.k + j) * kUnitKeys;   // keys of this unit the row sees
+                    const int vis = lim - (k0 + j) * kUnitKeys;   // keys of this unit the row sees
                     const bool part = __any_sync(0xffffffffu, vis < kUnitKeys);
                     uint32_t v[4][32];
 #pragma unroll
@@ -473,14 +514,14 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                     }
                     tmem_wait_st();
                 }
-                const int unit = s.k + j, valid = s.t.keys - unit * kUnitKeys;
+                const int unit = k0 + j, valid = keys - unit * kUnitKeys;
                 if (unit >= masked || valid < kUnitKeys) {
                     // V as the product may use it (both streams of a tall tile do the same)
-                    const uint32_t item = 2 * (unit0 + (uint32_t)j) + 1;
+                    const uint32_t item = item0 + 2 * (uint32_t)j + 1;
                     wait(&sm.kv_full[item % RING], (item / RING) & 1);
                     if (ok) {
                         unsigned char *vt = sm.kv[item % RING];
-                        const int r0 = unit >= masked ? max(s.t.base + 1 - unit * kUnitKeys, 0) : kUnitKeys;
+                        const int r0 = unit >= masked ? max(s.base + 1 - unit * kUnitKeys, 0) : kUnitKeys;
                         clean_values<D>(vt, r0, min(valid, kUnitKeys), row, fix[min(max(unit - masked, 0), kFixUnits - 1)]);
                     }
                 }
@@ -488,7 +529,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 mbar_arrive(&sm.p_full[x]);
             }
             // ------------------------------------------------------ epilogue
-            const bool fixable = masked < s.k + s.n;
+            const bool fixable = masked < k0 + n;
             if (joint) {
                 sm.ml[x][row] = make_float2(m_used, l);
                 wait(&sm.o_full[0], on[0] & 1);
@@ -521,7 +562,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                     w1 = ex2f(s1.x - ref);
                     l = w0 * s0.y + w1 * s1.y;
                 }
-                const size_t th = (size_t)(s.t.tok0 + tk) * a.Hq + (size_t)s.g * a.G + (r - tk * a.G);
+                const size_t th = (size_t)(s.tok0 + tk) * a.Hq + (size_t)s.g * a.G + (r - tk * a.G);
                 const float inv = s.direct ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
                 // of two streams, each writes half of the columns
                 const int c_lo = two ? x * (D / 2) : 0, c_hi = two ? c_lo + D / 2 : D;
@@ -552,7 +593,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                                 const int key = masked * kUnitKeys + 32 * f + __ffs(bits) - 1;
                                 bits &= bits - 1;
                                 if (key >= lim) continue;
-                                const int id = a.table[(size_t)s.t.owner * a.max_pages + (key >> a.shift)];
+                                const int id = a.table[(size_t)s.owner * a.max_pages + (key >> a.shift)];
                                 if (id < 0 || id >= a.n_pages) continue;
                                 const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(a.v_pages) +
                                     ((((long long)id * a.Hkv + s.g) << a.shift) + (key & (a.S - 1))) * D + c0;

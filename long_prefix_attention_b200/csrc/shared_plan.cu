@@ -130,6 +130,7 @@ shared_plan_kernel(const PlanArgs a) {
     };
     // ---- the tiles, and the cost before each (chunks of one tile a thread)
     long long before = 0;
+    int tall = 0;
     for (int c = 0; c < ntiles; c += kPlanThreads) {
         const int i = c + tid;
         Tile t{};
@@ -161,11 +162,13 @@ shared_plan_kernel(const PlanArgs a) {
         const long long inc = plan_scan(cost, warp_v, 0, tot, add);
         t.cost0 = before + inc - cost;
         before += tot;
+        tall |= t.ntok * G > kTileRows;
         if (i < ntiles) tiles[i] = t;
     }
     const long long W = before * a.Hkv;
     long long range = (W + a.workers - 1) / a.workers;
-    range = range < kCostMax ? kCostMax : range;  // a range holds the start of a unit of every pair it crosses
+    const int dearest = cost_unit(__syncthreads_or(tall) ? kDualRows : kTileRows);
+    range = range < dearest ? dearest : range;
     if (range > INT32_MAX) range = INT32_MAX;     // a table cannot be that long
     // ---- partial rows before each tile
     before = 0;
