@@ -136,6 +136,13 @@ __device__ __forceinline__ int first_masked_unit(const Tile &t) {
     return (t.flags & kLocal) ? min(max(t.base + 1, 0) / kUnitKeys, t.units) : t.units;
 }
 
+// Scores of places from n on: -inf.
+__device__ __forceinline__ void mask32(uint32_t (&v)[32], int n) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (i >= n) v[i] = 0xff800000u;
+}
+
 // Clears the places [r1, 128) of a V tile, and the non-finite values of keys
 // [r0, r1), whose bits are set in `fix`; 128 threads.
 template <int D>
@@ -438,67 +445,30 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 if (warp_live) {
                     const int vis = lim - (k0 + j) * kUnitKeys;   // keys of this unit the row sees
                     const bool part = __any_sync(0xffffffffu, vis < kUnitKeys);
-                    uint32_t v[4][32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(t_s + (uint32_t)(32 * c), v[c]);
-                    tmem_wait_ld();
-                    if (part) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (32 * c + i >= vis) v[c][i] = 0xff800000u;  // -inf
-                    }
-                    float mc[4];
-#pragma unroll
+                    // pass 1: the largest score
+                    float mraw = kNegInf;
+#pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32(t_s + (uint32_t)(32 * c), v);
+                        tmem_wait_ld();
+                        if (part) mask32(v, vis - 32 * c);
                         float m11[11];
 #pragma unroll
                         for (int i = 0; i < 10; ++i)
-                            m11[i] = max3_nan(__uint_as_float(v[c][3 * i]), __uint_as_float(v[c][3 * i + 1]),
-                                              __uint_as_float(v[c][3 * i + 2]));
-                        m11[10] = max_nan(__uint_as_float(v[c][30]), __uint_as_float(v[c][31]));
-                        mc[c] = max3_nan(max3_nan(max3_nan(m11[0], m11[1], m11[2]), max3_nan(m11[3], m11[4], m11[5]),
-                                                  max3_nan(m11[6], m11[7], m11[8])), m11[9], m11[10]);
+                            m11[i] = max3_nan(__uint_as_float(v[3 * i]), __uint_as_float(v[3 * i + 1]),
+                                              __uint_as_float(v[3 * i + 2]));
+                        m11[10] = max_nan(__uint_as_float(v[30]), __uint_as_float(v[31]));
+                        mraw = max3_nan(mraw, max3_nan(max3_nan(m11[0], m11[1], m11[2]), max3_nan(m11[3], m11[4], m11[5]),
+                                                       max3_nan(m11[6], m11[7], m11[8])), max_nan(m11[9], m11[10]));
                     }
-                    const float mt = max_nan(max3_nan(mc[0], mc[1], mc[2]), mc[3]) * sl2;
+                    const float mt = mraw * sl2;
                     float alpha = 1.f;
                     if (live && !(mt <= m_used + kRescale)) {   // a NaN passes, and stays
                         alpha = ex2f(m_used - mt);
                         m_used = mt;
                         l *= alpha;
                     }
-                    // p = 2^(s scale log2(e) - m), rounded to bf16 for the product with V
-                    // (the sum keeps fp32); P goes over the columns of S
-                    const float ref = m_used == kNegInf ? 0.f : m_used;
-                    const uint64_t sl2x2 = pack_f32x2(sl2, sl2), negm2 = pack_f32x2(-ref, -ref);
-                    uint64_t acc[4] = {0, 0, 0, 0};
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t pk[16];
-                        if (part) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const uint64_t t2 = fma_f32x2(pack_u32x2(v[c][2 * i], v[c][2 * i + 1]), sl2x2, negm2);
-                                const uint64_t p2 = pack_f32x2(ex2f(lo_f32(t2)), ex2f(hi_f32(t2)));
-                                acc[i & 3] = add_f32x2(acc[i & 3], p2);
-                                pk[i] = pack_bf16(lo_f32(p2), hi_f32(p2));
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const uint64_t t2 = fma_f32x2(pack_u32x2(v[c][2 * i], v[c][2 * i + 1]), sl2x2, negm2);
-                                uint64_t p2;
-                                if ((i & 3) == 3) p2 = exp2_poly_x2(t2);
-                                else p2 = pack_f32x2(ex2f(lo_f32(t2)), ex2f(hi_f32(t2)));
-                                acc[i & 3] = add_f32x2(acc[i & 3], p2);
-                                pk[i] = pack_bf16(lo_f32(p2), hi_f32(p2));
-                            }
-                        }
-                        tmem_st16(t_s + (uint32_t)(16 * c), pk);
-                    }
-                    const uint64_t a01 = add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3]));
-                    l += lo_f32(a01) + hi_f32(a01);
                     // tensor-memory access is warp-wide: rows that keep their maximum scale by 1
                     if (j > j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                         const uint32_t t_o = tmem + lane_off + (uint32_t)(x * 128);
@@ -512,6 +482,40 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                             tmem_st32(t_o + (uint32_t)c0, o);
                         }
                     }
+                    // pass 2: p = 2^(s scale log2(e) - m), rounded to bf16 for the product
+                    // with V (the sum keeps fp32); P goes over columns of S already read
+                    const float ref = m_used == kNegInf ? 0.f : m_used;
+                    const uint64_t sl2x2 = pack_f32x2(sl2, sl2), negm2 = pack_f32x2(-ref, -ref);
+                    uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32], pk[16];
+                        tmem_ld32(t_s + (uint32_t)(32 * c), v);
+                        tmem_wait_ld();
+                        if (part) {
+                            mask32(v, vis - 32 * c);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const uint64_t t2 = fma_f32x2(pack_u32x2(v[2 * i], v[2 * i + 1]), sl2x2, negm2);
+                                const uint64_t p2 = pack_f32x2(ex2f(lo_f32(t2)), ex2f(hi_f32(t2)));
+                                acc[i & 3] = add_f32x2(acc[i & 3], p2);
+                                pk[i] = pack_bf16(lo_f32(p2), hi_f32(p2));
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const uint64_t t2 = fma_f32x2(pack_u32x2(v[2 * i], v[2 * i + 1]), sl2x2, negm2);
+                                uint64_t p2;
+                                if ((i & 3) == 3) p2 = exp2_poly_x2(t2);
+                                else p2 = pack_f32x2(ex2f(lo_f32(t2)), ex2f(hi_f32(t2)));
+                                acc[i & 3] = add_f32x2(acc[i & 3], p2);
+                                pk[i] = pack_bf16(lo_f32(p2), hi_f32(p2));
+                            }
+                        }
+                        tmem_st16(t_s + (uint32_t)(16 * c), pk);
+                    }
+                    const uint64_t a01 = add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3]));
+                    l += lo_f32(a01) + hi_f32(a01);
                     tmem_wait_st();
                 }
                 const int unit = k0 + j, valid = keys - unit * kUnitKeys;
