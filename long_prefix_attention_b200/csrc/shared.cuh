@@ -1,10 +1,13 @@
 // shared.cuh -- the plan of a shared-prefix attention call: what the plan
 // kernel writes and the attention and merge kernels read.
 //
-// A tile is a run of tokens of one row (its local pages) or of one prefix
-// group (the group's prefix pages) with the G query heads of a KV head: at
-// most 128 query rows, or 256 when the run is longer than that.  A unit is
-// 128 keys of one tile for one KV head.  The (tile, KV head) pairs, tile by
+// A tile is a run of tokens with the G query heads of a KV head: at most 128
+// query rows, or 256 when the run is longer than that.  Its keys are those of
+// a prefix, or a row's own, or both: a row with more than 128 query rows fills
+// its tiles by itself, so they hold the prefix and the local keys and no
+// state has to be joined; the shorter rows between such rows share prefix
+// tiles, and each has a tile of its local keys.  A unit is 128 prefix or 128
+// local keys of one tile for one KV head.  The (tile, KV head) pairs, tile by
 // tile and head by head, are laid end to end by their cost and the line is
 // cut into equal ranges, one per worker (CTA): the work is balanced whatever
 // the lengths are, and a long key list is split as far as there are workers.
@@ -25,17 +28,17 @@ constexpr int kMagic = 0x53504c4e;
 
 struct __align__(16) Tile {
     int tok0, ntok;    // tokens of the batch
-    int owner;         // row (local) or group (prefix)
-    int flags;         // kLocal / kDirect
-    int keys;          // keys the tile's last token sees
-    int base;          // local: keys that lie before the token tok0 itself
-    int units;         // ceil(keys / kUnitKeys)
+    int group, row;    // prefix and row of its keys
+    int pre_keys;      // prefix keys (they come first)
+    int keys;          // local keys the last token sees
+    int base;          // local keys before the token tok0 itself
+    int units;         // ceil(pre_keys / kUnitKeys) + ceil(keys / kUnitKeys)
+    int direct;        // the tile holds all keys of its tokens
     int cap;           // segments at most, per KV head
     long long cost0;   // cost of all tiles before, for one KV head
     long long row0;    // partial rows of all tiles before
+    int pad[2];
 };
-constexpr int kLocal = 1;   // keys in the row's own pages, causal
-constexpr int kDirect = 2;  // the tile holds all keys of its tokens
 
 // Cost of a tile for one KV head: COST_HEAD for its queries and its epilogue,
 // then so much per unit.  A 256-row unit costs about twice a 128-row one (the
@@ -51,6 +54,7 @@ struct Header {
     int magic, R, NG, T, Hq, Hkv, page_size, max_pages, max_prefix_pages, workers, ntiles;
     int range;         // cost per worker
     long long W;       // cost of all (tile, KV head) pairs
+    double inv_range;
 };
 
 // Byte offsets in the plan buffer.
@@ -61,7 +65,9 @@ struct PlanLayout {
 inline __host__ __device__ long long max_tiles(int R, int NG, int T, int G) {
     const long long rows = R < T ? R : T, groups = NG < T ? NG : T;
     const long long full = ((long long)T * G + kDualRows - 1) / kDualRows;
-    return rows + groups + 2 * full;
+    // a local and a prefix tile for every row and group with tokens, the full
+    // ones, and the runs that rows of more than 128 query rows cut off
+    return rows + groups + 4 * full;
 }
 inline __host__ __device__ PlanLayout plan_layout(int R, int NG, int T, int G) {
     PlanLayout p;
@@ -94,7 +100,7 @@ struct AttnArgs {
     const Header *hdr;
     const int *first;         // [workers]
     const Tile *tiles;
-    const int2 *tok;          // [T] (local tile, prefix tile) of a token, -1 for none
+    const int2 *tok;          // [T] (the tile with its local keys, its prefix tile), -1 for none
     const void *q;            // [T][Hq][d]
     const void *k_pages, *v_pages;  // [n_pages][Hkv][S][d]
     const int *table;         // [R][max_pages]
@@ -114,13 +120,19 @@ __device__ __forceinline__ bool plan_ok(const AttnArgs &a, const Header &h) {
            h.page_size == a.S && h.workers == a.workers && h.max_pages == a.max_pages && h.max_prefix_pages == a.max_prefix_pages;
 }
 
+__device__ __forceinline__ int div_range(long long c, const Header &h) {
+    int q = (int)((double)c * h.inv_range);   // off by one at most: c < 2^53
+    if ((long long)q * h.range > c) --q;
+    else if ((long long)(q + 1) * h.range <= c) ++q;
+    return q;
+}
 // Worker that has the unit k of a pair whose cost begins at c0.
-__device__ __forceinline__ int worker_of(long long c0, int rows, int k, int range) {
-    return (int)((c0 + cost_head(rows) + (long long)cost_unit(rows) * k) / range);
+__device__ __forceinline__ int worker_of(long long c0, int rows, int k, const Header &h) {
+    return div_range(c0 + cost_head(rows) + (long long)cost_unit(rows) * k, h);
 }
 // Segments of a pair.
-__device__ __forceinline__ int segments(long long c0, int rows, int units, int range) {
-    return units > 0 ? worker_of(c0, rows, units - 1, range) - worker_of(c0, rows, 0, range) + 1 : 0;
+__device__ __forceinline__ int segments(long long c0, int rows, int units, const Header &h) {
+    return units > 0 ? worker_of(c0, rows, units - 1, h) - worker_of(c0, rows, 0, h) + 1 : 0;
 }
 
 // Partial states: the statistics of a segment's rows follow one another; its
@@ -139,13 +151,14 @@ struct Seg {
 };
 struct Walk {
     long long c, end;     // cost: where the current pair begins, where the range ends
-    int w, i, g, range, last, Hkv, G;
+    int w, i, g, last, Hkv, G;
+    const Header &h;
     const Tile *tiles;
     Tile t, next;
-    __device__ Walk(const AttnArgs &a, const Header &h, int w_)
-        : w(w_), g(0), range(h.range), last(h.ntiles - 1), Hkv(a.Hkv), G(a.G), tiles(a.tiles) {
-        const long long begin = (long long)w * range;
-        end = min(h.W, begin + range);
+    __device__ Walk(const AttnArgs &a, const Header &h_, int w_)
+        : w(w_), g(0), last(h_.ntiles - 1), Hkv(a.Hkv), G(a.G), h(h_), tiles(a.tiles) {
+        const long long begin = (long long)w * h.range;
+        end = min(h.W, begin + h.range);
         c = end;
         i = 0;
         if (begin < end) {
@@ -160,7 +173,7 @@ struct Walk {
     __device__ bool step(Seg &s) {
         while (c < end) {
             const int rows = t.ntok * G, cu = cost_unit(rows);
-            const long long u0 = c + cost_head(rows), lo = (long long)w * range;
+            const long long u0 = c + cost_head(rows), lo = (long long)w * h.range;
             // units that begin within [lo, end)
             const int k0 = lo <= u0 ? 0 : (int)((lo - u0 + cu - 1) / cu);
             const int k1 = t.units == 0 || end <= u0 ? 0 : (int)min((long long)t.units, (end - u0 + cu - 1) / cu);
@@ -170,8 +183,8 @@ struct Walk {
                 s.g = g;
                 s.k = k0;
                 s.n = k1 - k0;
-                s.direct = (t.flags & kDirect) && s.n == t.units;
-                s.prow = t.row0 + ((long long)g * t.cap + (w - worker_of(c, rows, 0, range))) * rows;
+                s.direct = t.direct && s.n == t.units;
+                s.prow = t.row0 + ((long long)g * t.cap + (w - worker_of(c, rows, 0, h))) * rows;
             }
             c += cost_of(rows, t.units);
             if (++g == Hkv) {

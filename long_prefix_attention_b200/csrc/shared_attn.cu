@@ -41,7 +41,7 @@ struct Smem {
 };
 
 template <int D>
-__device__ void load_keys(const AttnArgs &a, const Seg &s, int k1, int kb, const int *list, Smem<D> &sm) {
+__device__ void load_keys(const AttnArgs &a, int g, int kb, int k1, const int *list, Smem<D> &sm) {
     constexpr int LD = Smem<D>::LD, C = D / 4;
     const int tid = threadIdx.x;
     if (tid < kKB) {
@@ -61,7 +61,7 @@ __device__ void load_keys(const AttnArgs &a, const Seg &s, int k1, int kb, const
         const int r = i / C, c = (i - r * C) * 4, id = sm.page[r];
         float kx[4] = {0.f, 0.f, 0.f, 0.f}, vx[4] = {0.f, 0.f, 0.f, 0.f};
         if (id >= 0) {
-            const long long off = ((((long long)id * a.Hkv + s.g) << a.shift) + ((kb + r) & (a.S - 1))) * D + c;
+            const long long off = ((((long long)id * a.Hkv + g) << a.shift) + ((kb + r) & (a.S - 1))) * D + c;
             load_vec<float, 4>(static_cast<const float *>(a.k_pages) + off, kx);
             load_vec<float, 4>(static_cast<const float *>(a.v_pages) + off, vx);
         }
@@ -76,10 +76,9 @@ __device__ void run_segment(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
     constexpr int LD = Smem<D>::LD, LP = Smem<D>::LP, BR = 16 * MR, NC = D / 64;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int rows = s.t.ntok * a.G;
-    const int k0 = s.k * kUnitKeys, k1 = min((s.k + s.n) * kUnitKeys, s.t.keys);  // keys of the segment
-    const bool local = s.t.flags & kLocal;
-    const int *list = local ? a.table + (size_t)s.t.owner * a.max_pages
-                            : a.prefix_table + (size_t)s.t.owner * a.max_prefix_pages;
+    const int pu = (s.t.pre_keys + kUnitKeys - 1) / kUnitKeys;  // prefix units
+    const int *pre_list = a.prefix_table + (size_t)s.t.group * a.max_prefix_pages;
+    const int *own_list = a.table + (size_t)s.t.row * a.max_pages;
     for (int rb = 0; rb < rows; rb += BR) {
         __syncthreads();  // the previous rows' queries have been used
         for (int i = tid; i < BR * (D / 4); i += kThreads) {
@@ -93,19 +92,22 @@ __device__ void run_segment(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
             store_vec<float, 4>(sm.q + r * LD + c, x);
         }
         float m[MR], l[MR], o[MR][4 * NC];
-        int lim[MR];  // keys the row sees
+        int own[MR];  // local keys the row sees
 #pragma unroll
         for (int i = 0; i < MR; ++i) {
             m[i] = kNegInf;
             l[i] = 0.f;
             const int rr = rb + ty * MR + i;
-            lim[i] = min(k1, local ? s.t.base + rr / a.G + 1 : s.t.keys);
+            own[i] = min(s.t.keys, s.t.base + rr / a.G + 1);
 #pragma unroll
             for (int c = 0; c < 4 * NC; ++c) o[i][c] = 0.f;
         }
-        for (int kb = k0; kb < k1; kb += kKB) {
+        for (int hu = 2 * s.k; hu < 2 * (s.k + s.n); ++hu) {   // halves of units
+            const bool pre = hu < 2 * pu;
+            const int kb = (pre ? hu : hu - 2 * pu) * kKB, k1 = pre ? s.t.pre_keys : s.t.keys;
+            if (kb >= k1) continue;
             __syncthreads();
-            load_keys<D>(a, s, k1, kb, list, sm);
+            load_keys<D>(a, s.g, kb, k1, pre ? pre_list : own_list, sm);
             float sc[MR][4];
 #pragma unroll
             for (int i = 0; i < MR; ++i)
@@ -132,12 +134,13 @@ __device__ void run_segment(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
 #pragma unroll
             for (int i = 0; i < MR; ++i) {
                 float mx = kNegInf;
+                const int lim = pre ? k1 : own[i];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (kb + tx + 16 * j >= lim[i]) sc[i][j] = kNegInf;
+                    if (kb + tx + 16 * j >= lim) sc[i][j] = kNegInf;
                     mx = fmaxf(mx, sc[i][j]);
                 }
-                masked |= kb + kKB > lim[i];
+                masked |= kb + kKB > lim;
 #pragma unroll
                 for (int x = 8; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
                 const float mn = fmaxf(m[i], mx);
@@ -229,125 +232,175 @@ shared_attn_kernel(const AttnArgs a) {
 
 // ------------------------------------------------------------------ merge --
 //
-// NW warps per (token, query head): each reads its share of the partial
-// states (32 statistics at a time, then their rows, eight in flight), and the
-// warps meet in shared memory.  Pairs whose only state was written as output
-// already are skipped; pairs without any key get (0, -inf).
+// NW warps per (token, KV head), G query rows at once: the rows of one token
+// lie side by side in the partial states (16 bytes of each).  Lane l owns row
+// l % G and the 4-column groups l / G + k 32 / G; each warp takes every NW-th
+// state, four in flight, with running statistics, and the warps meet in shared
+// memory.  Tokens whose only state was written as output already are skipped;
+// tokens without any key get (0, -inf).  Bound by latency (offsets, tile,
+// statistics and states are read one after the other) for a few tokens, by
+// memory for many.
 
 constexpr int kMergeThreads = 256;
 
-template <typename T, int D, int NW>
+template <typename T, int D, int G, int NW>
 __global__ void __launch_bounds__(kMergeThreads)
 shared_merge_kernel(const AttnArgs a) {
-    constexpr int E = D / 32, PPB = kMergeThreads / 32 / NW;
-    __shared__ float so[NW > 1 ? PPB * NW : 1][D];
-    __shared__ float2 sml[NW > 1 ? PPB * NW : 1];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % NW, pb = warp / NW;
+    constexpr int C4 = D / 4, E = C4 * G < 32 ? 1 : C4 * G / 32;  // 4-column groups of a row, and per lane
+    constexpr int PPB = kMergeThreads / 32 / NW;         // pairs per block
+    __shared__ float4 so[NW > 1 ? kMergeThreads / 32 : 1][NW > 1 ? E : 1][32];
+    __shared__ float2 sml[NW > 1 ? kMergeThreads / 32 : 1][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % NW;
+    const int hh = lane % G, cg = lane / G;
+    const bool mine = C4 * G >= 32 || cg < C4;           // a row of 64 columns alone leaves half of the warp
+    pdl_wait();
+    pdl_launch_dependents();
     const Header h = *a.hdr;
     if (!plan_ok(a, h)) return;
-    const long long pairs = (long long)a.T * a.Hq;
+    const long long pairs = (long long)a.T * a.Hkv;
     for (long long base = (long long)blockIdx.x * PPB; base < pairs; base += (long long)gridDim.x * PPB) {
-        const long long pr = base + pb;
+        const long long pr = base + warp / NW;
         bool live = pr < pairs;
-        const int t = live ? (int)(pr / a.Hq) : 0, hq = live ? (int)(pr - (long long)t * a.Hq) : 0;
+        const int t = live ? (int)(pr / a.Hkv) : 0, g = live ? (int)(pr - (long long)t * a.Hkv) : 0;
         const int2 tt = live ? a.tok[t] : make_int2(-1, -1);
-        live = live && tt.x >= 0;  // tokens outside every row are left as they are
-        const int g = hq / a.G, hh = hq - g * a.G;
-        long long row[2] = {0, 0};            // first partial row of the pair's segments
-        int rows[2] = {0, 0}, at[2] = {0, 0}, n[2] = {0, 0};
+        live = live && tt.x >= 0;               // tokens outside every row are left as they are
+        // states of the two tiles: count, statistics and outputs of this lane's row, and their strides
+        int n[2] = {0, 0};
+        const float2 *ml[2] = {a.ws_ml, a.ws_ml};
+        const float4 *po[2] = {reinterpret_cast<const float4 *>(a.ws_o), reinterpret_cast<const float4 *>(a.ws_o)};
+        int rows[2] = {0, 0};
         if (live) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int i = x == 0 ? tt.x : tt.y;
                 if (i < 0) continue;
                 const Tile tl = a.tiles[i];
-                rows[x] = tl.ntok * a.G;
-                n[x] = segments(tl.cost0 * a.Hkv + g * cost_of(rows[x], tl.units), rows[x], tl.units, h.range);
-                if (x == 0 && n[x] == 1 && (tl.flags & kDirect)) live = false;  // already written
-                row[x] = tl.row0 + (long long)g * tl.cap * rows[x];
-                at[x] = (t - tl.tok0) * a.G + hh;
+                rows[x] = tl.ntok * G;
+                n[x] = segments(tl.cost0 * a.Hkv + g * cost_of(rows[x], tl.units), rows[x], tl.units, h);
+                if (x == 0 && n[x] == 1 && tl.direct) live = false;  // already written
+                const long long first = tl.row0 + (long long)g * tl.cap * rows[x];
+                const int at = (t - tl.tok0) * G + hh;
+                ml[x] += first + at;
+                po[x] += first * C4 + (long long)cg * rows[x] + at;
             }
         }
         const int tot = live ? n[0] + n[1] : 0;
-        float m = kNegInf, l = 0.f, o[E];
+        float m = kNegInf, l = 0.f;
+        float4 o[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = 0.f;
-        for (int e0 = sub * 32; e0 < tot; e0 += NW * 32) {
-            const int e = e0 + lane;
-            const long long r = e < n[0] ? row[0] + (long long)e * rows[0] + at[0]
-                                         : row[1] + (long long)(e - n[0]) * rows[1] + at[1];
-            const float2 ml = e < tot ? __ldcg(a.ws_ml + r) : make_float2(kNegInf, 0.f);
-            const float mn = fmaxf(m, warp_max(ml.x)), ref = mn == kNegInf ? 0.f : mn;
-            const float al = exp2f(m - ref), w = ml.y == 0.f ? 0.f : exp2f(ml.x - ref);
-            m = mn;
-            l = l * al + warp_sum(w * ml.y);
+        for (int k = 0; k < E; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int e0 = sub; e0 < tot; e0 += 4 * NW) {
+            float2 st[4];
+            float4 v[4][E];
 #pragma unroll
-            for (int d = 0; d < E; ++d) o[d] *= al;
-            const int cnt = min(32, tot - e0);
-            for (int j0 = 0; j0 < cnt; j0 += 8) {
-                float v[8][E];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int ee = e0 + min(j0 + j, cnt - 1);
-                    const float *p = a.ws_o + (ee < n[0] ? partial_at(row[0] + (long long)ee * rows[0], rows[0], at[0], lane * E, D)
-                                                         : partial_at(row[1] + (long long)(ee - n[0]) * rows[1], rows[1], at[1],
-                                                                      lane * E, D));
-#pragma unroll
-                    for (int d = 0; d < E; ++d) v[j][d] = __ldcg(p + d);
+            for (int j = 0; j < 4; ++j) {
+                const int e = e0 + j * NW;
+                if (e >= tot) {
+                    st[j] = make_float2(kNegInf, 0.f);
+                    continue;
                 }
+                const int x = e < n[0] ? 0 : 1, ee = x ? e - n[0] : e;
+                st[j] = __ldcg(ml[x] + (long long)ee * rows[x]);
+                const float4 *p = po[x] + (long long)ee * rows[x] * C4;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float wj = j0 + j < cnt ? __shfl_sync(0xffffffffu, w, (j0 + j) & 31) : 0.f;
-                    if (wj == 0.f) continue;  // an empty state's row may hold anything
+                for (int k = 0; k < E; ++k)
+                    v[j][k] = mine ? __ldcg(p + (long long)k * (32 / G) * rows[x]) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            float mn = m;
 #pragma unroll
-                    for (int d = 0; d < E; ++d) o[d] = fmaf(wj, v[j][d], o[d]);
+            for (int j = 0; j < 4; ++j) mn = fmaxf(mn, st[j].x);
+            const float ref = mn == kNegInf ? 0.f : mn, al = exp2f(m - ref);
+            m = mn;
+            l *= al;
+#pragma unroll
+            for (int k = 0; k < E; ++k) { o[k].x *= al; o[k].y *= al; o[k].z *= al; o[k].w *= al; }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (st[j].y == 0.f) continue;   // an empty state's row may hold anything
+                const float w = exp2f(st[j].x - ref);
+                l = fmaf(w, st[j].y, l);
+#pragma unroll
+                for (int k = 0; k < E; ++k) {
+                    o[k].x = fmaf(w, v[j][k].x, o[k].x);
+                    o[k].y = fmaf(w, v[j][k].y, o[k].y);
+                    o[k].z = fmaf(w, v[j][k].z, o[k].z);
+                    o[k].w = fmaf(w, v[j][k].w, o[k].w);
                 }
             }
         }
         if (NW > 1) {
             __syncthreads();
-            if (lane == 0) sml[warp] = make_float2(m, l);
+            sml[warp][lane] = make_float2(m, l);
 #pragma unroll
-            for (int d = 0; d < E; ++d) so[warp][lane * E + d] = o[d];
+            for (int k = 0; k < E; ++k) so[warp][k][lane] = o[k];
             __syncthreads();
             if (sub == 0) {
                 float mm = m;
-                for (int w = 1; w < NW; ++w) mm = fmaxf(mm, sml[warp + w].x);
+                for (int w = 1; w < NW; ++w) mm = fmaxf(mm, sml[warp + w][lane].x);
                 const float ref = mm == kNegInf ? 0.f : mm, al = exp2f(m - ref);
                 l *= al;
 #pragma unroll
-                for (int d = 0; d < E; ++d) o[d] *= al;
+                for (int k = 0; k < E; ++k) { o[k].x *= al; o[k].y *= al; o[k].z *= al; o[k].w *= al; }
                 for (int w = 1; w < NW; ++w) {
-                    const float x = exp2f(sml[warp + w].x - ref);
-                    l = fmaf(x, sml[warp + w].y, l);
+                    const float2 s2 = sml[warp + w][lane];
+                    const float x = exp2f(s2.x - ref);
+                    l = fmaf(x, s2.y, l);
 #pragma unroll
-                    for (int d = 0; d < E; ++d) o[d] = fmaf(x, so[warp + w][lane * E + d], o[d]);
+                    for (int k = 0; k < E; ++k) {
+                        const float4 y = so[warp + w][k][lane];
+                        o[k].x = fmaf(x, y.x, o[k].x);
+                        o[k].y = fmaf(x, y.y, o[k].y);
+                        o[k].z = fmaf(x, y.z, o[k].z);
+                        o[k].w = fmaf(x, y.w, o[k].w);
+                    }
                 }
                 m = mm;
             }
         }
-        if (live && sub == 0) {
+        if (live && sub == 0 && mine) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
+            const size_t th = (size_t)t * a.Hq + g * G + hh;
 #pragma unroll
-            for (int d = 0; d < E; ++d) o[d] *= inv;
-            store_vec<T, E>(static_cast<T *>(a.out) + (size_t)pr * D + lane * E, o);
-            if (a.lse && lane == 0) a.lse[pr] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+            for (int k = 0; k < E; ++k) {
+                const float y[4] = {o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv};
+                store_vec<T, 4>(static_cast<T *>(a.out) + th * D + 4 * (cg + k * (32 / G)), y);
+            }
+            if (a.lse && cg == 0) a.lse[th] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
         }
     }
 }
 
-template <typename T, int D>
+template <typename T, int D, int G>
 cudaError_t launch_merge(const AttnArgs &a, int num_sms, cudaStream_t st) {
-    // few pairs have many partial states each (the work is split further):
-    // eight warps a pair while the pairs do not fill the card, else one
-    const long long pairs = (long long)a.T * a.Hq;
-    if (pairs <= 8LL * num_sms) {
-        shared_merge_kernel<T, D, 8><<<(unsigned)pairs, kMergeThreads, 0, st>>>(a);
-    } else {
-        const long long blocks = (pairs + 7) / 8, most = 16LL * num_sms;
-        shared_merge_kernel<T, D, 1><<<(unsigned)(blocks < most ? blocks : most), kMergeThreads, 0, st>>>(a);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    // Few pairs have many states each (their keys are split further): eight
+    // warps a pair while the pairs leave most of the card empty, else one.
+    const long long pairs = (long long)a.T * a.Hkv;
+    if (pairs <= 4LL * num_sms) {
+        cfg.gridDim = dim3((unsigned)pairs);
+        return cudaLaunchKernelEx(&cfg, shared_merge_kernel<T, D, G, 8>, a);
     }
-    return cudaGetLastError();
+    const long long blocks = (pairs + 7) / 8, most = 32LL * num_sms;
+    cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most));
+    return cudaLaunchKernelEx(&cfg, shared_merge_kernel<T, D, G, 1>, a);
+}
+
+template <typename T, int D>
+cudaError_t merge_any(const AttnArgs &a, int num_sms, cudaStream_t st) {
+    switch (a.G) {
+        case 1: return launch_merge<T, D, 1>(a, num_sms, st);
+        case 2: return launch_merge<T, D, 2>(a, num_sms, st);
+        case 4: return launch_merge<T, D, 4>(a, num_sms, st);
+        case 8: return launch_merge<T, D, 8>(a, num_sms, st);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 template <int D>
@@ -359,14 +412,14 @@ cudaError_t launch_f32(const AttnArgs &a, int num_sms, cudaStream_t st) {
     kern<<<a.workers, kThreads, smem, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_merge<float, D>(a, num_sms, st);
+    return merge_any<float, D>(a, num_sms, st);
 }
 
 template <int D>
 cudaError_t launch_bf16(const AttnArgs &a, int num_sms, cudaStream_t st) {
     cudaError_t e = launch_attn_tc(a, num_sms, st);
     if (e != cudaSuccess) return e;
-    return launch_merge<__nv_bfloat16, D>(a, num_sms, st);
+    return merge_any<__nv_bfloat16, D>(a, num_sms, st);
 }
 
 }  // namespace shared

@@ -72,9 +72,9 @@ struct Cfg {
 constexpr int kSegs = 16;
 struct __align__(16) SegDesc {
     int tok0, rows, base, keys;      // first token, query rows; as in Tile
-    int g, k, n, flags;              // KV head, first unit, units; kLocal
+    int g, k, n, pre_keys;           // KV head, first unit, units; as in Tile
     long long prow;                  // first partial row
-    int owner, masked;               // row; first unit that some of the tile's rows see in part
+    int row, masked;                 // row; first unit that some of the tile's rows see in part
     int direct, pad[3];
 };
 
@@ -130,10 +130,12 @@ __device__ __forceinline__ void stream_sync(int x) {
     else asm volatile("bar.sync 3, 128;" ::: "memory");
 }
 
-// First unit (of the tile) that holds a key some row of the tile does not
-// see, when keys end at the row's own token; the tile's units if there is none.
+__device__ __forceinline__ int units_of(int keys) { return (keys + kUnitKeys - 1) / kUnitKeys; }
+
+// First unit (of the tile) that holds a local key some row of the tile does
+// not see, since it is a later token; the tile's units if there is none.
 __device__ __forceinline__ int first_masked_unit(const Tile &t) {
-    return (t.flags & kLocal) ? min(max(t.base + 1, 0) / kUnitKeys, t.units) : t.units;
+    return min(units_of(t.pre_keys) + max(t.base + 1, 0) / kUnitKeys, t.units);
 }
 
 // Scores of places from n on: -inf.
@@ -231,8 +233,8 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 SegDesc d{};
                 if (some) {
                     d.tok0 = s.t.tok0; d.rows = s.t.ntok * a.G; d.base = s.t.base; d.keys = s.t.keys;
-                    d.g = s.g; d.k = s.k; d.n = s.n; d.flags = s.t.flags & kLocal;
-                    d.prow = s.prow; d.owner = s.t.owner; d.masked = first_masked_unit(s.t); d.direct = s.direct;
+                    d.g = s.g; d.k = s.k; d.n = s.n; d.pre_keys = s.t.pre_keys;
+                    d.prow = s.prow; d.row = s.t.row; d.masked = first_masked_unit(s.t); d.direct = s.direct;
                 }
                 sm.seg[segs % kSegs] = d;
                 mbar_arrive(&sm.seg_full[segs % kSegs]);
@@ -267,17 +269,21 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 __syncwarp();
             }
             if (!dual) qb ^= 1;
-            const int *list = (s.t.flags & kLocal) ? a.table + (size_t)s.t.owner * a.max_pages
-                                                   : a.prefix_table + (size_t)s.t.owner * a.max_prefix_pages;
-            auto page = [&](int unit) {     // this lane's page of a unit
-                const int key = unit * kUnitKeys + lane * rows;
-                return (lane < boxes && unit < s.k + s.n && key < s.t.keys) ? list[key >> a.shift] : -1;
+            const int *pre_list = a.prefix_table + (size_t)s.t.group * a.max_prefix_pages;
+            const int *own_list = a.table + (size_t)s.t.row * a.max_pages;
+            const int pu = units_of(s.t.pre_keys);
+            auto page = [&](int unit, bool &used) {     // this lane's page of a unit
+                const bool pre = unit < pu;
+                const int key = (pre ? unit : unit - pu) * kUnitKeys + lane * rows;
+                used = lane < boxes && unit < s.k + s.n && key < (pre ? s.t.pre_keys : s.t.keys);
+                return used ? (pre ? pre_list : own_list)[key >> a.shift] : -1;
             };
-            int ahead = page(s.k);
+            bool next_used;
+            int ahead = page(s.k, next_used);
             for (int j = s.k; j < s.k + s.n && ok; ++j) {
                 const int id = ahead;
-                ahead = page(j + 1);
-                const bool used = lane < boxes && j * kUnitKeys + lane * rows < s.t.keys;
+                const bool used = next_used;
+                ahead = page(j + 1, next_used);
                 const bool bad = used && (id < 0 || id >= a.n_pages);
                 if (bad) set_error(a.ws_err, ASM_ERR_INVALID_ARG);
                 // past the cache (zero fill) for places behind the last key and bad ids
@@ -304,105 +310,108 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
         for (int x = 0; x < 2; ++x)
             if (qn[x] > 0 && !mbar_wait(&sm.q_full[x], (qn[x] - 1) & 1)) ok = false;
     } else if (warp == kIssuer) {
-        // ------------------------------------------------- MMA issuer
-        const uint32_t idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kUnitKeys >> 3) << 17) |
-                                 ((uint32_t)(128 >> 4) << 24);
-        const uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
-                                 ((uint32_t)(128 >> 4) << 24);
-        // Two cursors over the steps: the scores run two steps ahead of the
-        // outputs.  Step i belongs to stream i & 1.  A segment is kept as
-        // 2 units + (256-row tile); the outputs' cursor takes those that the
-        // scores' cursor has entered from a queue (two steps: two at most).
-        uint32_t segs = 0;
-        auto fetch = [&]() {
-            wait(&sm.seg_full[segs % kSegs], (segs / kSegs) & 1);
-            const SegDesc &d = sm.seg[segs++ % kSegs];
-            return ok && d.n > 0 ? 2 * d.n + (d.rows > kTileRows ? 1 : 0) : 0;
-        };
-        int s_seg = fetch(), p_seg = s_seg, q0 = 0, q1 = 0;
-        uint32_t s_step = 0, s_unit = 0, p_step = 0, p_unit = 0;   // steps and units before the cursor
-        int s_j = 0, s_half = 0, p_j = 0, p_half = 0;              // unit of the segment, step of a 256-row unit
-        uint32_t q_bits = 0;       // phases of the query buffers
-        int qb = 0;                // buffer of the next small tile
-        auto issue_s = [&]() {
-            const bool dual = s_seg & 1;
-            const int x = s_step & 1, b = dual ? x : qb;
-            // the first step on a query buffer waits for it, the last frees it
-            if (s_j == 0) {
-                wait(&sm.q_full[b], (q_bits >> b) & 1);
-                q_bits ^= 1u << b;
-            }
-            const uint32_t slot = (2 * s_unit) % RING;
-            if (s_half == 0) wait(&sm.kv_full[slot], ((2 * s_unit) / RING) & 1);
-            if (!ok) return;
-            tc_fence_after();
-            const bool last = s_j == (s_seg >> 1) - 1, done = !dual || s_half == 1;
-            if (lane == 0) {
-                const uint32_t qa = smem_addr(sm.q[b]), ka = smem_addr(sm.kv[slot]);
+        // ------------------------------------------------- MMA issuer (one lane)
+        if (lane == 0) {
+            const uint32_t idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kUnitKeys >> 3) << 17) |
+                                     ((uint32_t)(128 >> 4) << 24);
+            const uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
+                                     ((uint32_t)(128 >> 4) << 24);
+            // Two cursors over the steps: the scores run two steps ahead of the
+            // outputs.  Step i belongs to stream i & 1.  A segment is kept as
+            // 2 units + (256-row tile); the outputs' cursor takes those that the
+            // scores' cursor has entered from a queue (two steps: two at most).
+            // addresses within a descriptor add up: all of shared memory lies below 2^18
+            const uint64_t q_desc = desc_k_sw128(smem_addr(sm.q[0])), k_desc = desc_k_sw128(smem_addr(sm.kv[0])),
+                           v_desc = desc_mn_sw128(smem_addr(sm.kv[0]), kBox);
+            auto wait1 = [&](uint64_t *bar, uint32_t parity) { ok = ok && mbar_wait(bar, parity); };
+            uint32_t segs = 0;
+            auto fetch = [&]() {
+                wait1(&sm.seg_full[segs % kSegs], (segs / kSegs) & 1);
+                const SegDesc &d = sm.seg[segs++ % kSegs];
+                return ok && d.n > 0 ? 2 * d.n + (d.rows > kTileRows ? 1 : 0) : 0;
+            };
+            int s_seg = fetch(), p_seg = s_seg, q0 = 0, q1 = 0;
+            uint32_t s_step = 0, s_unit = 0, p_step = 0, p_unit = 0;   // steps and units before the cursor
+            int s_j = 0, s_half = 0, p_j = 0, p_half = 0;              // unit of the segment, step of a 256-row unit
+            uint32_t q_bits = 0;       // phases of the query buffers
+            int qb = 0;                // buffer of the next small tile
+            auto issue_s = [&]() {
+                const bool dual = s_seg & 1;
+                const int x = s_step & 1, b = dual ? x : qb;
+                // the first step on a query buffer waits for it, the last frees it
+                if (s_j == 0) {
+                    wait1(&sm.q_full[b], (q_bits >> b) & 1);
+                    q_bits ^= 1u << b;
+                }
+                const uint32_t slot = (2 * s_unit) % RING;
+                if (s_half == 0) wait1(&sm.kv_full[slot], ((2 * s_unit) / RING) & 1);
+                if (!ok) return;
+                tc_fence_after();
+                const bool last = s_j == (s_seg >> 1) - 1, done = !dual || s_half == 1;
+                const uint64_t qd = q_desc + (uint32_t)b * (C::TILE >> 4), kd = k_desc + slot * (C::TILE >> 4);
+                const uint32_t ts = tmem + 256 + (uint32_t)(x * 128);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (uint32_t)((kk >> 2) * kBox + (kk & 3) * 32);
-                    umma_bf16(tmem + 256 + (uint32_t)(x * 128), desc_k_sw128(qa + off), desc_k_sw128(ka + off), idesc_s,
-                              kk > 0 ? 1u : 0u);
+                    constexpr uint32_t box = kBox >> 4;
+                    const uint32_t off = (uint32_t)(kk >> 2) * box + (uint32_t)(kk & 3) * 2;
+                    umma_bf16(ts, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
                 }
                 umma_commit(&sm.s_full[x]);
                 if (done) umma_commit(&sm.kv_empty[slot]);
                 if (last) umma_commit(&sm.q_empty[b]);
-            }
-            __syncwarp();
-            ++s_step;
-            if (!done) {
-                s_half = 1;
-                return;
-            }
-            s_half = 0;
-            ++s_unit;
-            ++s_j;
-            if (last) {
-                if (!dual) qb ^= 1;
-                s_j = 0;
-                s_seg = fetch();
-                if (q0 == 0) q0 = s_seg;
-                else q1 = s_seg;
-            }
-        };
-        for (int i = 0; i < 2 && ok && s_seg != 0; ++i) issue_s();
-        uint32_t p_bits = 0;       // phases of the streams' P tiles
-        while (ok && p_seg != 0) {
-            const bool dual = p_seg & 1;
-            const int x = p_step & 1, n = p_seg >> 1;
-            const uint32_t item = 2 * p_unit + 1, slot = item % RING;
-            if (p_half == 0) wait(&sm.kv_full[slot], (item / RING) & 1);
-            wait(&sm.p_full[x], (p_bits >> x) & 1);
-            p_bits ^= 1u << x;
-            if (!ok) break;
-            tc_fence_after();
-            const bool done = !dual || p_half == 1;
-            if (lane == 0) {
-                const uint32_t va = smem_addr(sm.kv[slot]);
+                ++s_step;
+                if (!done) {
+                    s_half = 1;
+                    return;
+                }
+                s_half = 0;
+                ++s_unit;
+                ++s_j;
+                if (last) {
+                    if (!dual) qb ^= 1;
+                    s_j = 0;
+                    s_seg = fetch();
+                    if (q0 == 0) q0 = s_seg;
+                    else q1 = s_seg;
+                }
+            };
+            for (int i = 0; i < 2 && ok && s_seg != 0; ++i) issue_s();
+            uint32_t p_bits = 0;       // phases of the streams' P tiles
+            while (ok && p_seg != 0) {
+                const bool dual = p_seg & 1;
+                const int x = p_step & 1, n = p_seg >> 1;
+                const uint32_t item = 2 * p_unit + 1, slot = item % RING;
+                if (p_half == 0) wait1(&sm.kv_full[slot], (item / RING) & 1);
+                wait1(&sm.p_full[x], (p_bits >> x) & 1);
+                p_bits ^= 1u << x;
+                if (!ok) break;
+                tc_fence_after();
+                const bool done = !dual || p_half == 1;
+                const uint64_t vd = v_desc + slot * (C::TILE >> 4);
+                const uint32_t to = tmem + (uint32_t)(x * 128), tp = to + 256;
                 const bool fresh = dual ? p_j == 0 : p_j < 2;   // the stream's first step of the segment
 #pragma unroll
                 for (int kk = 0; kk < kUnitKeys / 16; ++kk)
                     // 16 keys a step: 8 tensor-memory columns of P, 16 rows of V
-                    umma_bf16_ts(tmem + (uint32_t)(x * 128), tmem + 256 + (uint32_t)(x * 128 + kk * 8),
-                                 desc_mn_sw128(va + (uint32_t)(kk * 2048), kBox), idesc_o, (!fresh || kk > 0) ? 1u : 0u);
+                    umma_bf16_ts(to, tp + (uint32_t)(kk * 8), vd + (uint32_t)(kk * (2048 >> 4)), idesc_o,
+                                 (!fresh || kk > 0) ? 1u : 0u);
                 if (dual ? p_j == n - 1 : p_j >= n - 2) umma_commit(&sm.o_full[x]);
                 if (done) umma_commit(&sm.kv_empty[slot]);
-            }
-            __syncwarp();
-            ++p_step;
-            p_half = done ? 0 : 1;
-            if (done) {
-                ++p_unit;
-                if (++p_j == n) {
-                    p_j = 0;
-                    p_seg = q0;
-                    q0 = q1;
-                    q1 = 0;
+                ++p_step;
+                p_half = done ? 0 : 1;
+                if (done) {
+                    ++p_unit;
+                    if (++p_j == n) {
+                        p_j = 0;
+                        p_seg = q0;
+                        q0 = q1;
+                        q1 = 0;
+                    }
                 }
+                if (s_seg != 0) issue_s();
             }
-            if (s_seg != 0) issue_s();
         }
+        __syncwarp();
     } else {
         // ----------------------------------------------------- softmax
         const int x = warp >> 2;            // stream
@@ -435,7 +444,8 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
             const bool live = r < rows;
             const bool warp_live = (dual ? x * 128 : 0) + qd * 32 < rows;
             const int tk = r / a.G;
-            const int lim = live && (s.flags & kLocal) ? min(s.base + tk + 1, keys) : keys;
+            const int pre_keys = s.pre_keys, pu = units_of(pre_keys);
+            const int own = live ? min(s.base + tk + 1, keys) : keys;   // local keys the row sees
             uint32_t(&fix)[kFixUnits][4] = sm.fix[seg & 3];
             float m_used = kNegInf, l = 0.f;
             for (int j = j0; j < n; j += dj) {
@@ -443,7 +453,8 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 ++sn;
                 tc_fence_after();
                 if (warp_live) {
-                    const int vis = lim - (k0 + j) * kUnitKeys;   // keys of this unit the row sees
+                    const int vis = k0 + j < pu ? pre_keys - (k0 + j) * kUnitKeys
+                                                : own - (k0 + j - pu) * kUnitKeys;   // keys of this unit the row sees
                     const bool part = __any_sync(0xffffffffu, vis < kUnitKeys);
                     // pass 1: the largest score
                     float mraw = kNegInf;
@@ -518,14 +529,15 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                     l += lo_f32(a01) + hi_f32(a01);
                     tmem_wait_st();
                 }
-                const int unit = k0 + j, valid = keys - unit * kUnitKeys;
+                const int unit = k0 + j, key0 = (unit < pu ? unit : unit - pu) * kUnitKeys;
+                const int valid = (unit < pu ? pre_keys : keys) - key0;
                 if (unit >= masked || valid < kUnitKeys) {
                     // V as the product may use it (both streams of a tall tile do the same)
                     const uint32_t item = item0 + 2 * (uint32_t)j + 1;
                     wait(&sm.kv_full[item % RING], (item / RING) & 1);
                     if (ok) {
                         unsigned char *vt = sm.kv[item % RING];
-                        const int r0 = unit >= masked ? max(s.base + 1 - unit * kUnitKeys, 0) : kUnitKeys;
+                        const int r0 = unit >= masked ? max(s.base + 1 - key0, 0) : kUnitKeys;
                         clean_values<D>(vt, r0, min(valid, kUnitKeys), row, fix[min(max(unit - masked, 0), kFixUnits - 1)]);
                     }
                 }
@@ -594,10 +606,10 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                         for (int f = 0; f < kFixUnits * 4; ++f) {
                             uint32_t bits = fix[f >> 2][f & 3];
                             while (bits) {
-                                const int key = masked * kUnitKeys + 32 * f + __ffs(bits) - 1;
+                                const int key = (masked - pu) * kUnitKeys + 32 * f + __ffs(bits) - 1;
                                 bits &= bits - 1;
-                                if (key >= lim) continue;
-                                const int id = a.table[(size_t)s.owner * a.max_pages + (key >> a.shift)];
+                                if (key >= own) continue;
+                                const int id = a.table[(size_t)s.row * a.max_pages + (key >> a.shift)];
                                 if (id < 0 || id >= a.n_pages) continue;
                                 const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(a.v_pages) +
                                     ((((long long)id * a.Hkv + s.g) << a.shift) + (key & (a.S - 1))) * D + c0;

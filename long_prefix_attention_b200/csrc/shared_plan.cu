@@ -2,8 +2,8 @@
 // GPU from the step's lengths.
 //
 // One block: running maxima make the offsets monotone whatever they hold,
-// then three sums over the rows, the groups and the tiles give the tile list,
-// the cost before each tile and the partial rows before each tile.  Bound by
+// then sums over the rows, the runs of rows that share prefix tiles and the
+// tiles give the tile list, the cost and the partial rows before each tile.  Bound by
 // latency; a step's layers share one plan.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -82,7 +82,9 @@ shared_plan_kernel(const PlanArgs a) {
     extern __shared__ int sm[];
     __shared__ long long warp_v[32];
     const int R = a.R, NG = a.NG, tid = threadIdx.x, G = a.Hq / a.Hkv;
-    int *qo = sm, *row_end = qo + R + 1, *go = row_end + R, *group_end = go + NG + 1;
+    // offsets; tiles up to and with each row's and each run's; a row's run, a run's first and last row
+    int *qo = sm, *go = qo + R + 1, *row_end = go + NG + 1, *run_end = row_end + R, *run_of = run_end + R,
+        *run_lo = run_of + R, *run_hi = run_lo + R;
     const PlanLayout lay = plan_layout(R, NG, a.T, G);
     Header *hdr = reinterpret_cast<Header *>(a.plan);
     int *first = reinterpret_cast<int *>(a.plan + lay.first);
@@ -94,40 +96,57 @@ shared_plan_kernel(const PlanArgs a) {
 
     monotone(a.q_off, qo, R, a.T, warp_v);
     if (NG > 0) monotone(a.group_off, go, NG, R, warp_v);
-    // tiles of n tokens: one of up to 128 rows, else 256-row ones
+    // tiles of n tokens: one of up to 128 query rows, else 256-row ones
     auto n_tiles = [&](int n) { return n <= 0 ? 0 : n <= single ? 1 : (n + dual - 1) / dual; };
-    // groups first: theirs are the long key lists
-    long long tot, n_prefix = 0;
-    if (NG > 0) {
-        const int per = (NG + kPlanThreads - 1) / kPlanThreads, i0 = tid * per;
-        long long s = 0;
-        for (int i = i0; i < i0 + per && i < NG; ++i) s += n_tiles(qo[go[i + 1]] - qo[go[i]]);
-        long long e = plan_scan(s, warp_v, 0, n_prefix, add) - s;
-        for (int i = i0; i < i0 + per && i < NG; ++i) {
-            e += n_tiles(qo[go[i + 1]] - qo[go[i]]);
-            group_end[i] = (int)e;
-        }
-    }
-    {
-        const int per = (R + kPlanThreads - 1) / kPlanThreads, i0 = tid * per;
-        long long s = 0;
-        for (int i = i0; i < i0 + per && i < R; ++i) s += n_tiles(qo[i + 1] - qo[i]);
-        long long e = n_prefix + plan_scan(s, warp_v, 0, tot, add) - s;
-        for (int i = i0; i < i0 + per && i < R; ++i) {
-            e += n_tiles(qo[i + 1] - qo[i]);
-            row_end[i] = (int)e;
-        }
-    }
-    __syncthreads();
-    const int ntiles = (int)(n_prefix + tot);
-    // group of a row (-1: none) and its prefix length
-    auto prefix_of = [&](int r) {
+    // group of a row, -1 for none
+    auto group_of = [&](int r) {
         if (NG == 0 || r < go[0] || r >= go[NG]) return -1;
         return first_above(go + 1, NG, r);
     };
     auto prefix_keys = [&](int g) {
         return (int)min((long long)max(a.prefix_len[g], 0), (long long)a.max_prefix_pages * a.S);
     };
+    auto tall_row = [&](int r) { return qo[r + 1] - qo[r] > single; };
+    // a run: neighbouring rows of one group, none of them tall
+    auto starts_run = [&](int r, int g) {
+        return g >= 0 && !tall_row(r) && (r == go[g] || tall_row(r - 1));
+    };
+    const int per = (R + kPlanThreads - 1) / kPlanThreads, r0 = tid * per, r1 = min(r0 + per, R);
+    long long tot, n_runs, n_prefix;
+    {
+        long long s = 0;
+        for (int r = r0; r < r1; ++r) s += starts_run(r, group_of(r));
+        long long e = plan_scan(s, warp_v, 0, n_runs, add) - s;
+        for (int r = r0; r < r1; ++r) {
+            const int g = group_of(r);
+            if (starts_run(r, g)) run_lo[e++] = r;
+            const bool in = g >= 0 && !tall_row(r);
+            run_of[r] = in ? (int)e - 1 : -1;
+            if (in && (r + 1 == go[g + 1] || tall_row(r + 1))) run_hi[e - 1] = r + 1;
+        }
+    }
+    __syncthreads();
+    // prefix tiles come first: theirs are the long key lists
+    {
+        long long s = 0;
+        for (int i = r0; i < min(r0 + per, (int)n_runs); ++i) s += n_tiles(qo[run_hi[i]] - qo[run_lo[i]]);
+        long long e = plan_scan(s, warp_v, 0, n_prefix, add) - s;
+        for (int i = r0; i < min(r0 + per, (int)n_runs); ++i) {
+            e += n_tiles(qo[run_hi[i]] - qo[run_lo[i]]);
+            run_end[i] = (int)e;
+        }
+    }
+    {
+        long long s = 0;
+        for (int r = r0; r < r1; ++r) s += n_tiles(qo[r + 1] - qo[r]);
+        long long e = n_prefix + plan_scan(s, warp_v, 0, tot, add) - s;
+        for (int r = r0; r < r1; ++r) {
+            e += n_tiles(qo[r + 1] - qo[r]);
+            row_end[r] = (int)e;
+        }
+    }
+    __syncthreads();
+    const int ntiles = (int)(n_prefix + tot);
     // ---- the tiles, and the cost before each (chunks of one tile a thread)
     long long before = 0;
     int tall = 0;
@@ -136,27 +155,31 @@ shared_plan_kernel(const PlanArgs a) {
         Tile t{};
         if (i < ntiles) {
             if (i < n_prefix) {
-                const int g = first_above(group_end, NG, i);
-                const int t0 = qo[go[g]], n = qo[go[g + 1]] - t0, per = n <= single ? n : dual;
-                const int j = i - (g > 0 ? group_end[g - 1] : 0);
-                t.tok0 = t0 + j * per;
-                t.ntok = min(per, n - j * per);
-                t.owner = g;
-                t.keys = prefix_keys(g);
+                const int q = first_above(run_end, (int)n_runs, i), g = group_of(run_lo[q]);
+                const int t0 = qo[run_lo[q]], n = qo[run_hi[q]] - t0, len = n <= single ? n : dual;
+                const int j = i - (q > 0 ? run_end[q - 1] : 0);
+                t.tok0 = t0 + j * len;
+                t.ntok = min(len, n - j * len);
+                t.group = g;
+                t.pre_keys = prefix_keys(g);
             } else {
-                const int r = first_above(row_end, R, i);
-                const int t0 = qo[r], n = qo[r + 1] - t0, per = n <= single ? n : dual;
+                const int r = first_above(row_end, R, i), g = group_of(r);
+                const int t0 = qo[r], n = qo[r + 1] - t0, len = n <= single ? n : dual;
                 const int j = i - (r > 0 ? row_end[r - 1] : (int)n_prefix);
-                const int len = (int)min((long long)max(a.seq_len[r], 0), (long long)a.max_pages * a.S);
-                t.tok0 = t0 + j * per;
-                t.ntok = min(per, n - j * per);
-                t.owner = r;
-                t.base = len - n + j * per;
-                t.keys = min(max(t.base + t.ntok, 0), len);
-                const int g = prefix_of(r);
-                t.flags = kLocal | ((g < 0 || prefix_keys(g) == 0) ? kDirect : 0);
+                const int seq = (int)min((long long)max(a.seq_len[r], 0), (long long)a.max_pages * a.S);
+                t.tok0 = t0 + j * len;
+                t.ntok = min(len, n - j * len);
+                t.row = r;
+                t.base = seq - n + j * len;
+                t.keys = min(max(t.base + t.ntok, 0), seq);
+                const int pre = g >= 0 ? prefix_keys(g) : 0;
+                if (n > single && g >= 0) {
+                    t.group = g;
+                    t.pre_keys = pre;
+                }
+                t.direct = pre == 0 || n > single;
             }
-            t.units = (t.keys + kUnitKeys - 1) / kUnitKeys;
+            t.units = (t.pre_keys + kUnitKeys - 1) / kUnitKeys + (t.keys + kUnitKeys - 1) / kUnitKeys;
         }
         const long long cost = cost_of(t.ntok * G, t.units);
         const long long inc = plan_scan(cost, warp_v, 0, tot, add);
@@ -197,10 +220,10 @@ shared_plan_kernel(const PlanArgs a) {
             const int r = first_above(qo + 1, R, t);
             const int n = qo[r + 1] - qo[r];
             v.x = (r > 0 ? row_end[r - 1] : (int)n_prefix) + (n <= single ? 0 : (t - qo[r]) / dual);
-            const int g = prefix_of(r);
-            if (g >= 0) {
-                const int gn = qo[go[g + 1]] - qo[go[g]];
-                v.y = (g > 0 ? group_end[g - 1] : 0) + (gn <= single ? 0 : (t - qo[go[g]]) / dual);
+            const int q = run_of[r];
+            if (q >= 0) {
+                const int t0 = qo[run_lo[q]], gn = qo[run_hi[q]] - t0;
+                v.y = (q > 0 ? run_end[q - 1] : 0) + (gn <= single ? 0 : (t - t0) / dual);
             }
         }
         tok[t] = v;
@@ -210,7 +233,7 @@ shared_plan_kernel(const PlanArgs a) {
         h.magic = kMagic;
         h.R = R; h.NG = NG; h.T = a.T; h.Hq = a.Hq; h.Hkv = a.Hkv;
         h.page_size = a.S; h.max_pages = a.max_pages; h.max_prefix_pages = a.max_prefix_pages;
-        h.workers = a.workers; h.ntiles = ntiles; h.range = (int)range; h.W = W;
+        h.workers = a.workers; h.ntiles = ntiles; h.range = (int)range; h.W = W; h.inv_range = 1.0 / (double)range;
         *hdr = h;
     }
 }
@@ -232,10 +255,10 @@ cudaError_t asm_shared_plan_launch(const int32_t *q_off, const int32_t *seq_len,
     a.S = page_size; a.max_pages = max_pages; a.max_prefix_pages = max_prefix_pages;
     a.workers = num_sms < kMaxWorkers ? num_sms : kMaxWorkers;
     a.plan = static_cast<char *>(plan);
-    const size_t smem = sizeof(int) * (2 * (size_t)R + 1 + 2 * (size_t)NG + 1);
+    const size_t smem = sizeof(int) * (6 * (size_t)R + (size_t)NG + 2);
     if (smem > 40 * 1024) {  // beside the static arrays
         cudaError_t e = cudaFuncSetAttribute(shared_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (4 * kMaxRows + 2) * (int)sizeof(int));
+                                             (7 * kMaxRows + 2) * (int)sizeof(int));
         if (e != cudaSuccess) return e;
     }
     shared_plan_kernel<<<1, kPlanThreads, smem, st>>>(a);
