@@ -10,7 +10,10 @@
 //              the page ids of a unit (one lane per page, read one unit ahead)
 //              and one TMA box per page and 64 columns, K and V tiles in turn
 //              through a ring that runs on across segments;
-//   warp 9     tensor memory; one lane issues the products;
+//   warp 9, 10 one lane each issues the products of stream 0 and of stream 1
+//              (an issuer's waits and address arithmetic run under the other
+//              stream's products; one issuer for both left the tensor pipe
+//              idle half of the time); warp 9 holds the tensor memory;
 //   warps 0-3  softmax stream 0, warps 4-7 softmax stream 1: a thread per
 //              query row (tensor-memory lane).  In units that end a tile's
 //              keys they also clear the places of V behind the last key, and
@@ -21,16 +24,16 @@
 // segments too.  A tile of more than 128 rows gives each stream 128 of its
 // rows, so a unit is two steps (one read of K and V serves 256 rows); in a
 // smaller one a unit is one step, and a segment of two or more units leaves a
-// state in both streams, which its epilogue joins.  The scores of step i + 2
-// are issued right behind the P V of step i, so one stream's softmax and
-// epilogue run under the other's products.
+// state in both streams, which its epilogue joins.  A stream's next scores are
+// issued right behind its P V, across segments too, so one stream's softmax
+// and epilogue run under the other's products.
 // Decode tiles with a few rows waste most of a product, which costs nothing:
 // a 128-key unit takes the tensor core 0.6 us and 64 KB take an SM's share of
 // HBM 1.5 us; warps without rows skip the softmax.
 // Tensor memory columns: O_0 [0,128) O_1 [128,256) S_0 / P_0 [256,384)
-// S_1 / P_1 [384,512).  Products complete in issue order, so S_x(next) (issued
-// after P_x V) overwrites P_x only once it was read, and its completion means
-// that O_x is stable.  Every wait is bounded; after a timeout a warp waits no
+// S_1 / P_1 [384,512).  A stream's products complete in issue order, so S_x(next)
+// (issued after P_x V) overwrites P_x only once it was read, and its completion
+// means that O_x is stable.  Every wait is bounded; after a timeout a warp waits no
 // more, keeps to the barriers it shares with others, and the error word is set.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -49,13 +52,14 @@ namespace tc {
 
 using namespace umma;
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr int kProducer = 8, kIssuer = 9;
 constexpr int kSoftmax = 256;       // threads of the two softmax streams
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.f;
 constexpr int kBox = 128 * 128;     // 128 rows x 64 columns of bf16
 constexpr int kFixUnits = 4;        // units of a tile that some of its rows see in part
+constexpr int kFix = 8;             // one stream is at most RING / 2 + 1 segments ahead of the other
 constexpr int kSmallRows = 32;      // query rows of the small box
 
 template <int D>
@@ -84,9 +88,9 @@ struct Smem {
     unsigned char kv[Cfg<D>::RING][Cfg<D>::TILE];
     SegDesc seg[kSegs];
     float2 ml[2][128];                 // a row's (max, sum) in each stream
-    uint32_t fix[4][kFixUnits][4];     // per segment (modulo 4): keys whose V was cleared, from the first masked unit on
+    uint32_t fix[kFix][kFixUnits][4];  // per segment (modulo kFix): keys whose V was cleared, from the first masked unit on
     uint64_t kv_full[Cfg<D>::RING], kv_empty[Cfg<D>::RING];
-    uint64_t seg_full[kSegs], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
+    uint64_t seg_full[kSegs], lag[Cfg<D>::RING / 2], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
     uint32_t tmem_base;
 };
 
@@ -188,19 +192,20 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
     if (tid == 0) {
         for (int i = 0; i < RING; ++i) {
             mbar_init(&sm.kv_full[i], 1);
-            mbar_init(&sm.kv_empty[i], 1);
+            mbar_init(&sm.kv_empty[i], 2);   // one arrival of each issuer, or two of one
         }
         for (int i = 0; i < kSegs; ++i) mbar_init(&sm.seg_full[i], 1);
+        for (int i = 0; i < RING / 2; ++i) mbar_init(&sm.lag[i], 1);
         for (int x = 0; x < 2; ++x) {
             mbar_init(&sm.q_full[x], 1);
-            mbar_init(&sm.q_empty[x], 1);
+            mbar_init(&sm.q_empty[x], 2);
             mbar_init(&sm.s_full[x], 1);
             mbar_init(&sm.p_full[x], 128);
             mbar_init(&sm.o_full[x], 1);
         }
         fence_mbar_init();
     }
-    if (tid < 4 * kFixUnits * 4) (&sm.fix[0][0][0])[tid] = 0;
+    if (tid < kFix * kFixUnits * 4) (&sm.fix[0][0][0])[tid] = 0;
     if (warp == kIssuer) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(smem_addr(&sm.tmem_base)), "r"(kTmemCols));
@@ -309,106 +314,104 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
             if (!mbar_wait(&sm.kv_full[i % RING], (i / RING) & 1)) ok = false;
         for (int x = 0; x < 2; ++x)
             if (qn[x] > 0 && !mbar_wait(&sm.q_full[x], (qn[x] - 1) & 1)) ok = false;
-    } else if (warp == kIssuer) {
-        // ------------------------------------------------- MMA issuer (one lane)
+    } else if (warp >= kIssuer) {
+        // ------------------------------------- product issuers (one lane each)
         if (lane == 0) {
+            const int x = warp - kIssuer;
             const uint32_t idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kUnitKeys >> 3) << 17) |
                                      ((uint32_t)(128 >> 4) << 24);
             const uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
                                      ((uint32_t)(128 >> 4) << 24);
-            // Two cursors over the steps: the scores run two steps ahead of the
-            // outputs.  Step i belongs to stream i & 1.  A segment is kept as
-            // 2 units + (256-row tile); the outputs' cursor takes those that the
-            // scores' cursor has entered from a queue (two steps: two at most).
             // addresses within a descriptor add up: all of shared memory lies below 2^18
             const uint64_t q_desc = desc_k_sw128(smem_addr(sm.q[0])), k_desc = desc_k_sw128(smem_addr(sm.kv[0])),
                            v_desc = desc_mn_sw128(smem_addr(sm.kv[0]), kBox);
+            const uint32_t t_o = tmem + (uint32_t)(x * 128), t_s = t_o + 256;
             auto wait1 = [&](uint64_t *bar, uint32_t parity) { ok = ok && mbar_wait(bar, parity); };
-            uint32_t segs = 0;
-            auto fetch = [&]() {
-                wait1(&sm.seg_full[segs % kSegs], (segs / kSegs) & 1);
-                const SegDesc &d = sm.seg[segs++ % kSegs];
-                return ok && d.n > 0 ? 2 * d.n + (d.rows > kTileRows ? 1 : 0) : 0;
-            };
-            int s_seg = fetch(), p_seg = s_seg, q0 = 0, q1 = 0;
-            uint32_t s_step = 0, s_unit = 0, p_step = 0, p_unit = 0;   // steps and units before the cursor
-            int s_j = 0, s_half = 0, p_j = 0, p_half = 0;              // unit of the segment, step of a 256-row unit
-            uint32_t q_bits = 0;       // phases of the query buffers
-            int qb = 0;                // buffer of the next small tile
-            auto issue_s = [&]() {
-                const bool dual = s_seg & 1;
-                const int x = s_step & 1, b = dual ? x : qb;
-                // the first step on a query buffer waits for it, the last frees it
-                if (s_j == 0) {
-                    wait1(&sm.q_full[b], (q_bits >> b) & 1);
-                    q_bits ^= 1u << b;
+            // this stream's steps: unit j of a segment of n, every dj-th
+            int n = 0, j = 0, dj = 1, qb = 0, next_qb = 0;
+            uint32_t segs = 0, step = 0, unit0 = 0;     // before the segment
+            uint32_t q_bits = 0;                        // phases of the query buffers
+            uint32_t lag_bits = 0;
+            bool dual = false;
+            auto next = [&]() {      // false behind the last step
+                j += dj;
+                while (j >= n) {
+                    step += (uint32_t)(dual ? 2 * n : n);
+                    unit0 += (uint32_t)n;
+                    wait1(&sm.seg_full[segs % kSegs], (segs / kSegs) & 1);
+                    const SegDesc &d = sm.seg[segs++ % kSegs];
+                    n = ok ? d.n : 0;
+                    if (n == 0) return false;
+                    dual = d.rows > kTileRows;
+                    dj = dual ? 1 : 2;
+                    j = dual ? 0 : (x ^ (int)(step & 1));
+                    // both streams follow the fills of both query buffers
+                    if (dual) {
+                        qb = x;
+                    } else {
+                        qb = next_qb;
+                        next_qb ^= 1;
+                    }
+                    if (j >= n) q_bits ^= 1u << qb;      // a single unit, on the other stream
+                    else if (dual) q_bits ^= 1u << (x ^ 1);
                 }
-                const uint32_t slot = (2 * s_unit) % RING;
-                if (s_half == 0) wait1(&sm.kv_full[slot], ((2 * s_unit) / RING) & 1);
+                return true;
+            };
+            auto issue_s = [&]() {
+                // A tall tile's second stream takes its scores when the first has found its
+                // maximum: left alone, the streams fall into step and the tensor cores
+                // idle during both softmaxes.  (The first can be ahead by the ring's units.)
+                if (dual && x == 1) {
+                    const int i = (unit0 + (uint32_t)j) % (RING / 2);
+                    wait1(&sm.lag[i], (lag_bits >> i) & 1);
+                    lag_bits ^= 1u << i;
+                }
+                if (j < dj) {        // the stream's first step of the segment
+                    wait1(&sm.q_full[qb], (q_bits >> qb) & 1);
+                    q_bits ^= 1u << qb;
+                }
+                const uint32_t item = 2 * (unit0 + (uint32_t)j), slot = item % RING;
+                wait1(&sm.kv_full[slot], (item / RING) & 1);
                 if (!ok) return;
                 tc_fence_after();
-                const bool last = s_j == (s_seg >> 1) - 1, done = !dual || s_half == 1;
-                const uint64_t qd = q_desc + (uint32_t)b * (C::TILE >> 4), kd = k_desc + slot * (C::TILE >> 4);
-                const uint32_t ts = tmem + 256 + (uint32_t)(x * 128);
+                const uint64_t qd = q_desc + (uint32_t)qb * (C::TILE >> 4), kd = k_desc + slot * (C::TILE >> 4);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     constexpr uint32_t box = kBox >> 4;
                     const uint32_t off = (uint32_t)(kk >> 2) * box + (uint32_t)(kk & 3) * 2;
-                    umma_bf16(ts, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
+                    umma_bf16(t_s, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
                 }
                 umma_commit(&sm.s_full[x]);
-                if (done) umma_commit(&sm.kv_empty[slot]);
-                if (last) umma_commit(&sm.q_empty[b]);
-                ++s_step;
-                if (!done) {
-                    s_half = 1;
-                    return;
-                }
-                s_half = 0;
-                ++s_unit;
-                ++s_j;
-                if (last) {
-                    if (!dual) qb ^= 1;
-                    s_j = 0;
-                    s_seg = fetch();
-                    if (q0 == 0) q0 = s_seg;
-                    else q1 = s_seg;
+                // a unit of a small tile has one issuer: it arrives for both
+                umma_commit(&sm.kv_empty[slot]);
+                if (!dual) mbar_arrive(&sm.kv_empty[slot]);
+                if (j + dj >= n) {
+                    umma_commit(&sm.q_empty[qb]);
+                    if (dual || n == 1) mbar_arrive(&sm.q_empty[qb]);
                 }
             };
-            for (int i = 0; i < 2 && ok && s_seg != 0; ++i) issue_s();
-            uint32_t p_bits = 0;       // phases of the streams' P tiles
-            while (ok && p_seg != 0) {
-                const bool dual = p_seg & 1;
-                const int x = p_step & 1, n = p_seg >> 1;
-                const uint32_t item = 2 * p_unit + 1, slot = item % RING;
-                if (p_half == 0) wait1(&sm.kv_full[slot], (item / RING) & 1);
-                wait1(&sm.p_full[x], (p_bits >> x) & 1);
-                p_bits ^= 1u << x;
+            uint32_t p_bit = 0;      // phase of the stream's P tiles
+            bool more = next();
+            if (more) issue_s();
+            while (ok && more) {
+                const uint32_t item = 2 * (unit0 + (uint32_t)j) + 1, slot = item % RING;
+                wait1(&sm.kv_full[slot], (item / RING) & 1);
+                wait1(&sm.p_full[x], p_bit);
+                p_bit ^= 1;
                 if (!ok) break;
                 tc_fence_after();
-                const bool done = !dual || p_half == 1;
                 const uint64_t vd = v_desc + slot * (C::TILE >> 4);
-                const uint32_t to = tmem + (uint32_t)(x * 128), tp = to + 256;
-                const bool fresh = dual ? p_j == 0 : p_j < 2;   // the stream's first step of the segment
+                const bool fresh = j < dj;
 #pragma unroll
                 for (int kk = 0; kk < kUnitKeys / 16; ++kk)
                     // 16 keys a step: 8 tensor-memory columns of P, 16 rows of V
-                    umma_bf16_ts(to, tp + (uint32_t)(kk * 8), vd + (uint32_t)(kk * (2048 >> 4)), idesc_o,
+                    umma_bf16_ts(t_o, t_s + (uint32_t)(kk * 8), vd + (uint32_t)(kk * (2048 >> 4)), idesc_o,
                                  (!fresh || kk > 0) ? 1u : 0u);
-                if (dual ? p_j == n - 1 : p_j >= n - 2) umma_commit(&sm.o_full[x]);
-                if (done) umma_commit(&sm.kv_empty[slot]);
-                ++p_step;
-                p_half = done ? 0 : 1;
-                if (done) {
-                    ++p_unit;
-                    if (++p_j == n) {
-                        p_j = 0;
-                        p_seg = q0;
-                        q0 = q1;
-                        q1 = 0;
-                    }
-                }
-                if (s_seg != 0) issue_s();
+                if (j + dj >= n) umma_commit(&sm.o_full[x]);
+                umma_commit(&sm.kv_empty[slot]);
+                if (!dual) mbar_arrive(&sm.kv_empty[slot]);
+                more = next();
+                if (more) issue_s();
             }
         }
         __syncwarp();
@@ -446,7 +449,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
             const int tk = r / a.G;
             const int pre_keys = s.pre_keys, pu = units_of(pre_keys);
             const int own = live ? min(s.base + tk + 1, keys) : keys;   // local keys the row sees
-            uint32_t(&fix)[kFixUnits][4] = sm.fix[seg & 3];
+            uint32_t(&fix)[kFixUnits][4] = sm.fix[seg % kFix];
             float m_used = kNegInf, l = 0.f;
             for (int j = j0; j < n; j += dj) {
                 wait(&sm.s_full[x], sn & 1);
@@ -500,6 +503,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                     uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
+                        if (c == 0 && dual && tid == 0) mbar_arrive(&sm.lag[(item0 / 2 + (uint32_t)j) % (RING / 2)]);
                         uint32_t v[32], pk[16];
                         tmem_ld32(t_s + (uint32_t)(32 * c), v);
                         tmem_wait_ld();
