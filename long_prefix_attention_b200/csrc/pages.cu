@@ -25,13 +25,18 @@ namespace pages {
 
 constexpr int kThreads = 512;
 constexpr int kMaxRows = 4096;
-constexpr int kPer = kMaxRows / kThreads;  // rows per thread at most
 
 struct Args {
     const int *kv_len, *new_len, *pos_base, *pool_state;
     int *pool, *table, *seq_len, *q_off, *row, *pos, *slot, *pool_out;
     int R, F, shift, max_pages, T;
 };
+
+// Place i of a ring of F from its place `head` on: head < F, i <= F.
+__device__ __forceinline__ int ring(int head, long long i, int F) {
+    const long long p = head + i;
+    return (int)(p >= F ? p - F : p);
+}
 
 // Inclusive sum over the block's threads in order; `tot` gets the total.
 __device__ __forceinline__ long long block_scan(long long v, long long *warp_sums, long long &tot) {
@@ -66,6 +71,8 @@ __device__ __forceinline__ int find_row(const int *ends, int R, int t) {
     return lo;
 }
 
+// PER: rows per thread at most.
+template <int PER>
 __global__ void __launch_bounds__(kThreads)
 page_step_kernel(const Args a) {
     extern __shared__ int sm[];
@@ -82,14 +89,14 @@ page_step_kernel(const Args a) {
     const int count = min(max(cnt0, 0), a.F);
     const int head = (int)((unsigned)max(head0, 0) % (unsigned)a.F);
 
-    // rows [r0, r0 + per) of this thread
-    const int per = (R + kThreads - 1) / kThreads, r0 = tid * per;
-    int kv[kPer], nw[kPer];
+    // rows [r0, r0 + PER) of this thread
+    const int r0 = tid * PER;
+    int kv[PER], nw[PER];
     long long sum = 0, tot;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
         const int r = r0 + i;
-        const bool in = i < per && r < R;
+        const bool in = r < R;
         const int k = in ? a.kv_len[r] : 0;
         kv[i] = (int)min((long long)max(k, 0), cap);
         nw[i] = in ? a.new_len[r] : 0;
@@ -97,13 +104,13 @@ page_step_kernel(const Args a) {
     }
     // ends of the rows' tokens in the batch
     long long end = block_scan(sum, warp_sums, tot) - sum;
-    long long need[kPer];
+    long long need[PER];
     unsigned fits = 0;
     sum = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
         end += max(nw[i], 0);
-        if (i < per && r0 + i < R) tok_end[r0 + i] = (int)min(end, (long long)a.T);
+        if (r0 + i < R) tok_end[r0 + i] = (int)min(end, (long long)a.T);
         const long long want = (long long)kv[i] + max(nw[i], 0);
         const bool f = nw[i] >= 0 && end <= a.T && want <= cap;
         fits |= (unsigned)f << i;
@@ -115,7 +122,7 @@ page_step_kernel(const Args a) {
     long long gives = 0, backs = 0;
     unsigned ok = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
         asked += need[i];
         const bool o = ((fits >> i) & 1u) && (need[i] == 0 || asked <= count);
         ok |= (unsigned)o << i;
@@ -128,9 +135,9 @@ page_step_kernel(const Args a) {
     n_back = min(n_back, (long long)(a.F - count));  // a ring cannot hold more than it has places
     int refused = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
         const int r = r0 + i;
-        if (!(i < per && r < R)) continue;
+        if (r >= R) continue;
         const bool o = (ok >> i) & 1u;
         if (o) ge += need[i];
         if (nw[i] < 0) be += ((long long)kv[i] + S1) >> a.shift;
@@ -145,7 +152,7 @@ page_step_kernel(const Args a) {
     if (blockIdx.x == 0) {
         for (int r = tid; r <= R; r += kThreads) a.q_off[r] = r == 0 ? 0 : tok_end[r - 1];
         if (tid == 0) {
-            a.pool_out[0] = (int)(((long long)head + n_give) % a.F);
+            a.pool_out[0] = ring(head, n_give, a.F);
             a.pool_out[1] = (int)(count - n_give + n_back);
             a.pool_out[2] = s_refused;
         }
@@ -154,7 +161,7 @@ page_step_kernel(const Args a) {
     // the page with index j of row r, whose first `held` pages were there before
     auto page_of = [&](int r, int j, int held, int gstart) {
         if (j < held) return a.table[(size_t)r * a.max_pages + j];
-        return a.pool[(int)(((long long)head + gstart + (j - held)) % a.F)];
+        return a.pool[ring(head, gstart + (j - held), a.F)];
     };
     const int step = gridDim.x * kThreads;
     for (int t = blockIdx.x * kThreads + tid; t < a.T; t += step) {
@@ -178,12 +185,24 @@ page_step_kernel(const Args a) {
     for (long long i = (long long)blockIdx.x * kThreads + tid; i < n_give; i += step) {
         const int r = find_row(give_end, R, (int)i), gs = r > 0 ? give_end[r - 1] : 0;
         const int c = kv_ok[r], held = (int)(((long long)(c < 0 ? ~c : c) + S1) >> a.shift);
-        a.table[(size_t)r * a.max_pages + held + ((int)i - gs)] = a.pool[(int)(((long long)head + i) % a.F)];
+        a.table[(size_t)r * a.max_pages + held + ((int)i - gs)] = a.pool[ring(head, i, a.F)];
     }
     for (long long i = (long long)blockIdx.x * kThreads + tid; i < n_back; i += step) {
         const int r = find_row(back_end, R, (int)i), j = (int)i - (r > 0 ? back_end[r - 1] : 0);
-        a.pool[(int)(((long long)head + count + i) % a.F)] = a.table[(size_t)r * a.max_pages + j];
+        a.pool[ring(head, count + i, a.F)] = a.table[(size_t)r * a.max_pages + j];
     }
+}
+
+template <int PER>
+cudaError_t launch(const Args &a, int blocks, cudaStream_t st) {
+    const size_t smem = sizeof(int) * 4 * (size_t)a.R;
+    if (smem > 40 * 1024) {  // beside the static arrays
+        cudaError_t e = cudaFuncSetAttribute(page_step_kernel<PER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             4 * kMaxRows * (int)sizeof(int));
+        if (e != cudaSuccess) return e;
+    }
+    page_step_kernel<PER><<<blocks, kThreads, smem, st>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace pages
@@ -202,17 +221,13 @@ cudaError_t asm_page_step_launch(const int32_t *kv_len, const int32_t *new_len, 
     a.R = R; a.F = F; a.max_pages = max_pages; a.T = T;
     a.shift = 0;
     while ((1 << a.shift) < page_size) ++a.shift;
-    const size_t smem = sizeof(int) * 4 * (size_t)R;
-    if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(page_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             4 * kMaxRows * (int)sizeof(int));
-        if (e != cudaSuccess) return e;
-    }
     // one token a thread, up to a block per SM; the moved pages are at most about as many
     int blocks = (T + kThreads - 1) / kThreads;
     const int by_rows = (R + 127) / 128;
     blocks = blocks > by_rows ? blocks : by_rows;
     blocks = blocks < num_sms ? blocks : num_sms;
-    page_step_kernel<<<blocks < 1 ? 1 : blocks, kThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    blocks = blocks < 1 ? 1 : blocks;
+    if (R <= kThreads) return launch<1>(a, blocks, st);
+    if (R <= 2 * kThreads) return launch<2>(a, blocks, st);
+    return launch<kMaxRows / kThreads>(a, blocks, st);
 }

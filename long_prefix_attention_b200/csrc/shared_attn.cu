@@ -217,6 +217,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 shared_attn_kernel(const AttnArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw);
+    pdl_wait();
+    pdl_launch_dependents();
     const Header h = *a.hdr;
     if (!plan_ok(a, h)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicExch(a.ws_err, (int)ASM_ERR_INVALID_ARG);
@@ -409,8 +411,17 @@ cudaError_t launch_f32(const AttnArgs &a, int num_sms, cudaStream_t st) {
     auto kern = shared_attn_kernel<D>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<a.workers, kThreads, smem, st>>>(a);
-    e = cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.workers);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, a);
     if (e != cudaSuccess) return e;
     return merge_any<float, D>(a, num_sms, st);
 }

@@ -320,34 +320,57 @@ def _want(fn: str, ok: bool) -> None:
         raise AsmError(fn, ASM_ERR_INVALID_ARG)
 
 
-def _on_device(fn: str, *ts) -> None:
-    """Every tensor on the current CUDA device (the stream's)."""
-    dev = None
-    for t in ts:
-        if t is None:
-            continue
-        if t.device.type != "cuda":
-            raise ValueError(f"{fn}: tensors must be on a CUDA device, got {t.device}")
-        if dev is None:
-            dev = t.device.index
-            if dev != torch.cuda.current_device():
-                raise ValueError(f"{fn}: tensors are on {t.device}, the current device is {torch.cuda.current_device()}")
-        elif t.device.index != dev:
-            raise ValueError(f"{fn}: tensors are on different devices")
+def _take(fn: str, want: tuple, more: tuple = ()) -> int:
+    """Every tensor on the current CUDA device, those of `want` contiguous;
+    returns the device.  One short pass: a decode step makes several of these
+    calls, and their host time is what a small one costs."""
+    dev = want[0].get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        _refuse(fn, want[0], -1)
+    for t in want:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            _refuse(fn, t, dev)
+    for t in more:
+        if t.get_device() != dev:
+            _refuse(fn, t, dev)
+    return dev
+
+
+def _refuse(fn: str, t, dev: int) -> None:
+    if t.device.type != "cuda":
+        raise ValueError(f"{fn}: tensors must be on a CUDA device, got {t.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{fn}: tensors must all be on the current device, got {t.device}")
+    raise ValueError(f"{fn}: tensors must be contiguous")
 
 
 def _i32(fn: str, *ts) -> None:
     for t in ts:
-        if t is not None and t.dtype != torch.int32:
+        if t is not None and t.dtype is not torch.int32:
             raise TypeError(f"{fn}: lengths, ids and positions must be int32, got {t.dtype}")
+
+
+def _f64(fn: str, t) -> None:
+    if t.dtype is not torch.float64:
+        raise TypeError(f"{fn}: freq must be float64, got {t.dtype}")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(dev: int, stream) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _heads(fn: str, t, T: int, d: int, dtype) -> tuple[int, int]:
     """Token and head strides of a [T, H, d] view whose heads are contiguous."""
-    _want(fn, t.dim() == 3 and t.shape[0] == T and t.shape[2] == d and t.dtype == dtype)
-    if t.stride(2) != 1:
+    st = t.stride()
+    if len(st) != 3 or t.shape[0] != T or t.shape[2] != d or t.dtype is not dtype:
+        raise AsmError(fn, ASM_ERR_INVALID_ARG)
+    if st[2] != 1:
         raise ValueError(f"{fn}: heads must be contiguous")
-    return t.stride(0), t.stride(1)
+    return st[0], st[1]
 
 
 def asm_page_step(kv_len, new_len, pool, pool_state, page_size: int, table, seq_len, q_off, row, pos, slot, pool_out,
@@ -356,29 +379,26 @@ def asm_page_step(kv_len, new_len, pool, pool_state, page_size: int, table, seq_
     (negative: the row ends).  table[R,max_pages] and the ring pool[F] are
     updated; seq_len[R], q_off[R+1], row/pos/slot[T] and pool_out[3] written."""
     fn = "asm_page_step"
-    ts = (kv_len, new_len, pos_base, pool, pool_state, table, seq_len, q_off, row, pos, slot, pool_out)
-    _on_device(fn, *ts)
-    _contig(*ts)
-    _i32(fn, *ts)
+    dev = _take(fn, (kv_len, new_len, pos_base, pool, pool_state, table, seq_len, q_off, row, pos, slot, pool_out))
+    _i32(fn, kv_len, new_len, pos_base, pool, pool_state, table, seq_len, q_off, row, pos, slot, pool_out)
     R, T = kv_len.numel(), row.numel()
     _want(fn, table.dim() == 2 and table.shape[0] == R and new_len.numel() == R and seq_len.numel() == R and
           q_off.numel() == R + 1 and pos.numel() == T and slot.numel() == T and pool_state.numel() == 3 and
           pool_out.numel() == 3 and (pos_base is None or pos_base.numel() == R))
     _check(fn, _lib.load().asm_page_step(
-        _p(kv_len), _p(new_len), _p(pos_base), R, int(page_size), table.shape[1], _p(table), _p(pool), _p(pool_state),
-        pool.numel(), T, _p(seq_len), _p(q_off), _p(row), _p(pos), _p(slot), _p(pool_out), _stream(stream)))
+        kv_len.data_ptr(), new_len.data_ptr(), _ptr(pos_base), R, page_size, table.shape[1], table.data_ptr(),
+        pool.data_ptr(), pool_state.data_ptr(), pool.numel(), T, seq_len.data_ptr(), q_off.data_ptr(), row.data_ptr(),
+        pos.data_ptr(), slot.data_ptr(), pool_out.data_ptr(), _raw_stream(dev, stream)))
 
 
 def asm_rope_freqs(freq, theta: float, scaling: int = ASM_ROPE_SCALE_NONE, factor: float = 1.0, lo: float = 1.0,
                    hi: float = 4.0, ctx: float = 8192.0, stream=None):
     """Angle per position of each rotated pair into freq[rot/2] (fp64)."""
-    _on_device("asm_rope_freqs", freq)
-    _contig(freq)
-    if freq.dtype != torch.float64:
-        raise TypeError(f"asm_rope_freqs: freq must be float64, got {freq.dtype}")
-    _check("asm_rope_freqs", _lib.load().asm_rope_freqs(
-        _p(freq), 2 * freq.numel(), float(theta), int(scaling), float(factor), float(lo), float(hi), float(ctx),
-        _stream(stream)))
+    fn = "asm_rope_freqs"
+    dev = _take(fn, (freq,))
+    _f64(fn, freq)
+    _check(fn, _lib.load().asm_rope_freqs(
+        freq.data_ptr(), 2 * freq.numel(), theta, scaling, factor, lo, hi, ctx, _raw_stream(dev, stream)))
 
 
 def asm_rope(x, pos, freq, y, layout: int = ASM_ROPE_HALF, mscale: float = 1.0, inverse: bool = False, stream=None):
@@ -386,17 +406,15 @@ def asm_rope(x, pos, freq, y, layout: int = ASM_ROPE_HALF, mscale: float = 1.0, 
     may be x; the first 2 * len(freq) elements of each head turn.  inverse
     turns back: the gradient of the call without it."""
     fn = "asm_rope"
-    _on_device(fn, x, pos, freq, y)
-    _contig(pos, freq)
+    dev = _take(fn, (pos, freq), (x, y))
     _i32(fn, pos)
-    if freq.dtype != torch.float64:
-        raise TypeError(f"{fn}: freq must be float64, got {freq.dtype}")
+    _f64(fn, freq)
     T, H, d = x.shape
     _want(fn, y.shape == x.shape and pos.numel() == T)
     xs, ys = _heads(fn, x, T, d, x.dtype), _heads(fn, y, T, d, x.dtype)
     _check(fn, _lib.load().asm_rope(
-        _p(x), *xs, T, H, d, _dt(x), _p(pos), _p(freq), 2 * freq.numel(), int(layout), float(mscale), int(bool(inverse)),
-        _p(y), *ys, _stream(stream)))
+        x.data_ptr(), *xs, T, H, d, _dt(x), pos.data_ptr(), freq.data_ptr(), 2 * freq.numel(), layout, mscale,
+        1 if inverse else 0, y.data_ptr(), *ys, _raw_stream(dev, stream)))
 
 
 def asm_rope_append(q, k, v, pos, slot, freq, q_out, k_pages, v_pages, layout: int = ASM_ROPE_HALF,
@@ -405,21 +423,21 @@ def asm_rope_append(q, k, v, pos, slot, freq, q_out, k_pages, v_pages, layout: i
     which goes with v to the tokens' slots of k_pages, v_pages
     [n_pages,Hkv,S,d]; slots outside the pages store nothing."""
     fn = "asm_rope_append"
-    _on_device(fn, q, k, v, pos, slot, freq, q_out, k_pages, v_pages)
-    _contig(pos, slot, freq, k_pages, v_pages)
+    dev = _take(fn, (pos, slot, freq, k_pages, v_pages), (q, k, v, q_out))
     _i32(fn, pos, slot)
-    if freq.dtype != torch.float64:
-        raise TypeError(f"{fn}: freq must be float64, got {freq.dtype}")
+    _f64(fn, freq)
     T, Hq, d = q.shape
     Hkv = k.shape[1]
+    pages = k_pages.shape
     _want(fn, q_out.shape == q.shape and v.shape == k.shape and pos.numel() == T and slot.numel() == T and
-          k_pages.dim() == 4 and k_pages.shape == v_pages.shape and k_pages.shape[1] == Hkv and
-          k_pages.shape[3] == d and k_pages.dtype == q.dtype and v_pages.dtype == q.dtype)
-    qs, ks, vs, os = (_heads(fn, t, T, d, q.dtype) for t in (q, k, v, q_out))
+          len(pages) == 4 and pages == v_pages.shape and pages[1] == Hkv and pages[3] == d and
+          k_pages.dtype is q.dtype and v_pages.dtype is q.dtype)
+    dt = q.dtype
+    qs, ks, vs, os = _heads(fn, q, T, d, dt), _heads(fn, k, T, d, dt), _heads(fn, v, T, d, dt), _heads(fn, q_out, T, d, dt)
     _check(fn, _lib.load().asm_rope_append(
-        _p(q), *qs, _p(k), *ks, _p(v), *vs, T, Hq, Hkv, d, _dt(q), _p(pos), _p(slot), _p(freq), 2 * freq.numel(),
-        int(layout), float(mscale), _p(q_out), *os, _p(k_pages), _p(v_pages), k_pages.shape[0], k_pages.shape[2],
-        _stream(stream)))
+        q.data_ptr(), *qs, k.data_ptr(), *ks, v.data_ptr(), *vs, T, Hq, Hkv, d, _dt(q), pos.data_ptr(), slot.data_ptr(),
+        freq.data_ptr(), 2 * freq.numel(), layout, mscale, q_out.data_ptr(), *os, k_pages.data_ptr(),
+        v_pages.data_ptr(), pages[0], pages[2], _raw_stream(dev, stream)))
 
 
 def asm_shared_plan_size(R: int, NG: int, T: int, Hq: int, Hkv: int) -> int:
@@ -432,9 +450,7 @@ def asm_shared_plan(q_off, seq_len, table, T: int, Hq: int, Hkv: int, page_size:
     seq_len[R], and the rows group_off[NG+1] that share each prefix of
     prefix_len[NG] tokens (the tables give the page limits only)."""
     fn = "asm_shared_plan"
-    ts = (q_off, seq_len, table, group_off, prefix_len, prefix_table, plan)
-    _on_device(fn, *ts)
-    _contig(*ts)
+    dev = _take(fn, (q_off, seq_len, table, group_off, prefix_len, prefix_table, plan))
     _i32(fn, q_off, seq_len, table, group_off, prefix_len, prefix_table)
     R = seq_len.numel()
     NG = 0 if group_off is None else group_off.numel() - 1
@@ -442,9 +458,9 @@ def asm_shared_plan(q_off, seq_len, table, T: int, Hq: int, Hkv: int, page_size:
     _want(fn, NG <= 0 or (prefix_len is not None and prefix_table is not None and prefix_len.numel() == NG and
                           prefix_table.dim() == 2 and prefix_table.shape[0] == NG))
     _check(fn, _lib.load().asm_shared_plan(
-        _p(q_off), _p(seq_len), _p(group_off), _p(prefix_len), R, NG, int(T), int(Hq), int(Hkv), int(page_size),
-        table.shape[1], prefix_table.shape[1] if NG > 0 else 0, _p(plan), plan.numel() * plan.element_size(),
-        _stream(stream)))
+        q_off.data_ptr(), seq_len.data_ptr(), _ptr(group_off), _ptr(prefix_len), R, NG, T, Hq, Hkv, page_size,
+        table.shape[1], prefix_table.shape[1] if NG > 0 else 0, plan.data_ptr(), plan.numel() * plan.element_size(),
+        _raw_stream(dev, stream)))
 
 
 def asm_shared_attention_workspace_size(T: int, Hq: int, Hkv: int, d: int) -> int:
@@ -456,21 +472,20 @@ def asm_shared_attention(q, k_pages, v_pages, table, plan, scale: float, out, ws
     """Attention of the tokens q[T,Hq,d] over their rows' shared prefixes and
     local pages [n_pages,Hkv,S,d] into out[T,Hq,d] (and lse_out[T,Hq])."""
     fn = "asm_shared_attention"
-    ts = (q, k_pages, v_pages, table, plan, out, ws, prefix_table, lse_out)
-    _on_device(fn, *ts)
-    _contig(*ts)
+    dev = _take(fn, (q, k_pages, v_pages, table, plan, out, ws, prefix_table, lse_out))
     _i32(fn, table, prefix_table)
     T, Hq, d = q.shape
-    n_pages, Hkv, S, _ = k_pages.shape
+    pages, dt = k_pages.shape, q.dtype
     NG = 0 if prefix_table is None else prefix_table.shape[0]
-    _want(fn, k_pages.shape == v_pages.shape and k_pages.shape[3] == d and out.shape == q.shape and
-          table.dim() == 2 and (prefix_table is None or prefix_table.dim() == 2) and out.dtype == q.dtype and
-          k_pages.dtype == q.dtype and v_pages.dtype == q.dtype)
-    _want(fn, lse_out is None or (lse_out.dtype == torch.float32 and lse_out.numel() == T * Hq))
+    _want(fn, len(pages) == 4 and pages == v_pages.shape and pages[3] == d and out.shape == q.shape and
+          table.dim() == 2 and (prefix_table is None or prefix_table.dim() == 2) and out.dtype is dt and
+          k_pages.dtype is dt and v_pages.dtype is dt)
+    _want(fn, lse_out is None or (lse_out.dtype is torch.float32 and lse_out.numel() == T * Hq))
     _check(fn, _lib.load().asm_shared_attention(
-        _p(q), _p(k_pages), _p(v_pages), n_pages, S, _p(table), table.shape[1], _p(prefix_table),
-        prefix_table.shape[1] if NG else 0, _p(plan), plan.numel() * plan.element_size(), table.shape[0], NG, T, Hq,
-        Hkv, d, float(scale), _dt(q), _p(out), _p(lse_out), _p(ws), ws.numel() * ws.element_size(), _stream(stream)))
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), pages[0], pages[2], table.data_ptr(), table.shape[1],
+        _ptr(prefix_table), prefix_table.shape[1] if NG else 0, plan.data_ptr(), plan.numel() * plan.element_size(),
+        table.shape[0], NG, T, Hq, pages[1], d, scale, _dt(q), out.data_ptr(), _ptr(lse_out), ws.data_ptr(),
+        ws.numel() * ws.element_size(), _raw_stream(dev, stream)))
 
 
 # ---------------------------------------------------------------- helpers --
