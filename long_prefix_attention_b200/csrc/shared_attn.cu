@@ -24,74 +24,274 @@ namespace shared {
 
 // ------------------------------------------------------- CUDA-core kernel --
 //
-// 64 keys at a time in shared memory as fp32; 16 x 16 threads, each with MR
-// query rows and 4 keys of S = Q K^T, then MR rows and D / 16 columns of
-// O += P V.  The 16 threads of a row share a half-warp, which keeps its
-// statistics and its row of P to itself.  MR = 1 (16 rows a block) serves
-// decode tiles, MR = 4 (64 rows) longer ones.
+// Half a unit, 64 keys, at a time in shared memory, the next half on its way
+// (cp.async, two buffers).  Tiles of up to 16 query rows (decode): four
+// threads share a 4 x 4 block of scores (a quarter of the products each), the
+// 16 threads of a row find its weights, and each half-warp adds 4 keys to a
+// whole 16 x D output, summed over the half-warps at the end; so K and V leave
+// shared memory once per half (64 rows of 2048 local keys: 139 us, a row-wise
+// split that waits for its loads 190).  Longer tiles take 64 rows at a time
+// with 4 x 4 scores a thread, which is bound by the FMA pipe; 17 to 64 rows
+// through the short path in turns of 16 measured slower (44 rows: 64 us
+// against 49).
+
+__device__ __forceinline__ float dot4(const float4 &x, const float4 &y, float t) {
+    t = fmaf(x.x, y.x, t);
+    t = fmaf(x.y, y.y, t);
+    t = fmaf(x.z, y.z, t);
+    return fmaf(x.w, y.w, t);
+}
+__device__ __forceinline__ void axpy4(float w, const float4 &v, float4 &o) {
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+}
+__device__ __forceinline__ void scale4(float f, float4 &o) {
+    o.x *= f;
+    o.y *= f;
+    o.z *= f;
+    o.w *= f;
+}
 
 constexpr int kThreads = 256;
-constexpr int kKB = 64;  // keys per block step
+constexpr int kKB = 64;   // keys per step
+constexpr int kFew = 16;  // query rows of a short tile
 
 template <int D>
 struct Smem {
-    static constexpr int LD = D + 4, LP = kKB + 4;
-    float q[64 * LD], k[kKB * LD], v[kKB * LD], p[64 * LP];
-    int page[kKB];
+    static constexpr int LD = D + 4, LQ = D + 16, LP = kKB + 4;
+    float q[64 * LQ], k[2][kKB * LD], v[2][kKB * LD];
+    float p[64 * LP];     // scores, then weights; few rows: weights by key, [kKB][kFew + 4]
+    float al[kFew];       // few rows: this step's factor on a row's output
+    float2 ml[kFew];      // few rows: a row's (max, sum)
 };
+static_assert(kKB * (kFew + 4) + kFew * (kKB + 4) <= 64 * (kKB + 4), "scores and weights of few rows");
 
-template <int D>
-__device__ void load_keys(const AttnArgs &a, int g, int kb, int k1, const int *list, Smem<D> &sm) {
-    constexpr int LD = Smem<D>::LD, C = D / 4;
-    const int tid = threadIdx.x;
-    if (tid < kKB) {
-        const int key = kb + tid;
-        int id = -1;
-        if (key < k1) {
-            id = list[key >> a.shift];
-            if (id < 0 || id >= a.n_pages) {
-                id = -1;
-                atomicExch(a.ws_err, (int)ASM_ERR_INVALID_ARG);
-            }
-        }
-        sm.page[tid] = id;
-    }
-    __syncthreads();
-    for (int i = tid; i < kKB * C; i += kThreads) {
-        const int r = i / C, c = (i - r * C) * 4, id = sm.page[r];
-        float kx[4] = {0.f, 0.f, 0.f, 0.f}, vx[4] = {0.f, 0.f, 0.f, 0.f};
-        if (id >= 0) {
-            const long long off = ((((long long)id * a.Hkv + g) << a.shift) + ((kb + r) & (a.S - 1))) * D + c;
-            load_vec<float, 4>(static_cast<const float *>(a.k_pages) + off, kx);
-            load_vec<float, 4>(static_cast<const float *>(a.v_pages) + off, vx);
-        }
-        store_vec<float, 4>(sm.k + r * LD + c, kx);
-        store_vec<float, 4>(sm.v + r * LD + c, vx);
-    }
-    __syncthreads();
+// Where the keys of the half unit `hu` of a segment lie.
+struct Half {
+    int kb, k1;           // first key; end of its list
+    const int *list;
+    bool pre;
+};
+__device__ __forceinline__ Half half_of(const AttnArgs &a, const Seg &s, int hu) {
+    const int pu = (s.t.pre_keys + kUnitKeys - 1) / kUnitKeys;  // prefix units
+    Half f;
+    f.pre = hu < 2 * pu;
+    f.kb = (f.pre ? hu : hu - 2 * pu) * kKB;
+    f.k1 = f.pre ? s.t.pre_keys : s.t.keys;
+    f.list = f.pre ? a.prefix_table + (size_t)s.t.group * a.max_prefix_pages
+                   : a.table + (size_t)s.t.row * a.max_pages;
+    return f;
 }
 
-template <int D, int MR>
-__device__ void run_segment(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
-    constexpr int LD = Smem<D>::LD, LP = Smem<D>::LP, BR = 16 * MR, NC = D / 64;
+// Start the copies of a half; places behind the list's end and of bad pages
+// become zeros.
+template <int D>
+__device__ __forceinline__ void start_keys(const AttnArgs &a, int g, const Half &f, float *k, float *v) {
+    constexpr int LD = Smem<D>::LD, C = D / 4, N = kKB * C / kThreads;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int e = threadIdx.x + i * kThreads, r = e / C, c = (e - r * C) * 4, key = f.kb + r;
+        int id = key < f.k1 ? f.list[key >> a.shift] : -1;
+        if (key < f.k1 && (id < 0 || id >= a.n_pages)) {
+            id = -1;
+            atomicExch(a.ws_err, (int)ASM_ERR_INVALID_ARG);
+        }
+        const long long off = id < 0 ? 0 : ((((long long)id * a.Hkv + g) << a.shift) + (key & (a.S - 1))) * D + c;
+        const uint32_t bytes = id < 0 ? 0u : 16u;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                     ::"r"(smem_addr(k + r * LD + c)), "l"(static_cast<const float *>(a.k_pages) + off), "r"(bytes)
+                     : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                     ::"r"(smem_addr(v + r * LD + c)), "l"(static_cast<const float *>(a.v_pages) + off), "r"(bytes)
+                     : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void wait_keys() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+template <int D>
+__device__ __forceinline__ void load_queries(const AttnArgs &a, const Seg &s, int rb, int n, int rows, float *q) {
+    for (int i = threadIdx.x; i < n * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), c = (i - r * (D / 4)) * 4, rr = rb + r;
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        if (rr < rows)
+            load_vec<float, 4>(static_cast<const float *>(a.q) +
+                                   ((size_t)(s.t.tok0 + rr / a.G) * a.Hq + s.g * a.G + rr % a.G) * D + c, x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] *= a.sl2;
+        store_vec<float, 4>(q + r * Smem<D>::LQ + c, x);
+    }
+}
+
+// One row's 4 columns of a finished segment: the output itself, or a partial state.
+template <int D>
+__device__ __forceinline__ void store_row(const AttnArgs &a, const Seg &s, int rows, int rr, int col, float4 o, float m,
+                                          float l, bool stats) {
+    if (s.direct) {
+        const size_t th = (size_t)(s.t.tok0 + rr / a.G) * a.Hq + s.g * a.G + rr % a.G;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + th * D + col) =
+            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (a.lse && stats) a.lse[th] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+    } else {
+        *reinterpret_cast<float4 *>(a.ws_o + partial_at(s.prow, rows, rr, col, D)) = o;
+        if (stats) a.ws_ml[s.prow + rr] = make_float2(m, l);
+    }
+}
+
+template <int D>
+__device__ void run_few(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
+    constexpr int LD = Smem<D>::LD, LQ = Smem<D>::LQ, LS = kKB + 4, LW = kFew + 4, NC = D / 64;
+    const int tid = threadIdx.x, tx = tid & 15, hw = tid >> 4;
+    const int rows = s.t.ntok * a.G;
+    float *sc = sm.p, *wt = sm.p + kFew * LS;        // [kFew][LS] scores, [kKB][LW] weights
+    // scores: places 4 (ds + 4 t) .. of rows r4 + 4 i and keys k16 + 16 j
+    const int ds = tid & 3, r4 = (tid >> 2) & 3, k16 = tid >> 4;
+    const int own = min(s.t.keys, s.t.base + hw / a.G + 1);   // weights: row hw
+    const int own_first = min(s.t.keys, s.t.base + 1);
+    float m = kNegInf, l = 0.f;
+    float4 o[kFew][NC];
+#pragma unroll
+    for (int r = 0; r < kFew; ++r)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) o[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();                                  // the segment before is done with the buffers
+    start_keys<D>(a, s.g, half_of(a, s, 2 * s.k), sm.k[0], sm.v[0]);
+    load_queries<D>(a, s, 0, kFew, rows, sm.q);
+    int buf = 0;
+    for (int hu = 2 * s.k; hu < 2 * (s.k + s.n); ++hu) {
+        const Half f = half_of(a, s, hu);
+        wait_keys();
+        __syncthreads();                              // this half is here, the other buffer free
+        if (hu + 1 < 2 * (s.k + s.n)) start_keys<D>(a, s.g, half_of(a, s, hu + 1), sm.k[buf ^ 1], sm.v[buf ^ 1]);
+        if (f.kb < f.k1) {
+            {
+                float t[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) t[i][j] = 0.f;
+#pragma unroll 4
+                for (int d = 4 * ds; d < D; d += 16) {
+                    float4 kx[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        kx[j] = *reinterpret_cast<const float4 *>(sm.k[buf] + (k16 + 16 * j) * LD + d);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 qx = *reinterpret_cast<const float4 *>(sm.q + (r4 + 4 * i) * LQ + d);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) t[i][j] = dot4(qx, kx[j], t[i][j]);
+                    }
+                }
+                // the four threads' sums: two rows, then one row each
+                const bool hi = ds & 2, odd = ds & 1;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float send = hi ? t[i][j] : t[i + 2][j], keep = hi ? t[i + 2][j] : t[i][j];
+                        t[i][j] = keep + __shfl_xor_sync(0xffffffffu, send, 2);
+                    }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float send = odd ? t[0][j] : t[1][j], keep = odd ? t[1][j] : t[0][j];
+                    sc[(r4 + 4 * ds) * LS + k16 + 16 * j] = keep + __shfl_xor_sync(0xffffffffu, send, 1);
+                }
+            }
+            __syncthreads();
+            {
+                const int lim = f.pre ? f.k1 : own;
+                float x[4], mx = kNegInf;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[j] = f.kb + tx + 16 * j < lim ? sc[hw * LS + tx + 16 * j] : kNegInf;
+                    mx = fmaxf(mx, x[j]);
+                }
+#pragma unroll
+                for (int i = 8; i >= 1; i >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
+                const float mn = fmaxf(m, mx), ref = mn == kNegInf ? 0.f : mn, al = exp2f(m - ref);
+                m = mn;
+                float ps = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p = exp2f(x[j] - ref);
+                    ps += p;
+                    wt[(tx + 16 * j) * LW + hw] = p;
+                }
+#pragma unroll
+                for (int i = 8; i >= 1; i >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, i);
+                l = l * al + ps;
+                if (tx == 0) sm.al[hw] = al;
+            }
+            __syncthreads();
+            // a weight of 0 at a key the row does not see must not meet its value
+            const bool masked = !f.pre && f.kb + kKB > own_first;
+#pragma unroll
+            for (int r = 0; r < kFew; ++r) {
+                const float al = sm.al[r];
+#pragma unroll
+                for (int c = 0; c < NC; ++c) scale4(al, o[r][c]);
+            }
+#pragma unroll 2
+            for (int i = 0; i < kKB / 16; ++i) {
+                const int kk = hw * (kKB / 16) + i;
+                float4 vx[NC];
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    vx[c] = *reinterpret_cast<const float4 *>(sm.v[buf] + kk * LD + 64 * c + 4 * tx);
+#pragma unroll
+                for (int r = 0; r < kFew; r += 4) {
+                    const float4 w4 = *reinterpret_cast<const float4 *>(wt + kk * LW + r);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float w = e == 0 ? w4.x : e == 1 ? w4.y : e == 2 ? w4.z : w4.w;
+                        if (masked && w == 0.f) continue;
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) axpy4(w, vx[c], o[r + e][c]);
+                    }
+                }
+            }
+        }
+        buf ^= 1;
+    }
+    // the half-warps' outputs meet in the key and value buffers
+    static_assert(16 * kFew * D <= 4 * kKB * Smem<D>::LD, "outputs of the half-warps fit the buffers");
+    float *all = sm.k[0];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kFew; ++r)
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            *reinterpret_cast<float4 *>(all + (hw * kFew + r) * D + 64 * c + 4 * tx) = o[r][c];
+    if (tx == 0) sm.ml[hw] = make_float2(m, l);
+    __syncthreads();
+    for (int i = tid; i < rows * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), col = (i - r * (D / 4)) * 4;
+        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int w = 0; w < 16; ++w) {
+            const float4 x = *reinterpret_cast<const float4 *>(all + (w * kFew + r) * D + col);
+            t.x += x.x; t.y += x.y; t.z += x.z; t.w += x.w;
+        }
+        const float2 ml = sm.ml[r];
+        store_row<D>(a, s, rows, r, col, t, ml.x, ml.y, col == 0);
+    }
+}
+
+template <int D>
+__device__ void run_many(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
+    constexpr int LD = Smem<D>::LD, LQ = Smem<D>::LQ, LP = Smem<D>::LP, MR = 4, BR = 16 * MR, NC = D / 64;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int rows = s.t.ntok * a.G;
-    const int pu = (s.t.pre_keys + kUnitKeys - 1) / kUnitKeys;  // prefix units
-    const int *pre_list = a.prefix_table + (size_t)s.t.group * a.max_prefix_pages;
-    const int *own_list = a.table + (size_t)s.t.row * a.max_pages;
     for (int rb = 0; rb < rows; rb += BR) {
-        __syncthreads();  // the previous rows' queries have been used
-        for (int i = tid; i < BR * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), c = (i - r * (D / 4)) * 4, rr = rb + r;
-            float x[4] = {0.f, 0.f, 0.f, 0.f};
-            if (rr < rows)
-                load_vec<float, 4>(static_cast<const float *>(a.q) +
-                                       ((size_t)(s.t.tok0 + rr / a.G) * a.Hq + s.g * a.G + rr % a.G) * D + c, x);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] *= a.sl2;
-            store_vec<float, 4>(sm.q + r * LD + c, x);
-        }
-        float m[MR], l[MR], o[MR][4 * NC];
+        __syncthreads();  // the previous rows are done with the buffers
+        start_keys<D>(a, s.g, half_of(a, s, 2 * s.k), sm.k[0], sm.v[0]);
+        load_queries<D>(a, s, rb, BR, rows, sm.q);
+        float m[MR], l[MR];
+        float4 o[MR][NC];
         int own[MR];  // local keys the row sees
 #pragma unroll
         for (int i = 0; i < MR; ++i) {
@@ -100,14 +300,19 @@ __device__ void run_segment(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
             const int rr = rb + ty * MR + i;
             own[i] = min(s.t.keys, s.t.base + rr / a.G + 1);
 #pragma unroll
-            for (int c = 0; c < 4 * NC; ++c) o[i][c] = 0.f;
+            for (int c = 0; c < NC; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
+        int buf = 1;
         for (int hu = 2 * s.k; hu < 2 * (s.k + s.n); ++hu) {   // halves of units
-            const bool pre = hu < 2 * pu;
-            const int kb = (pre ? hu : hu - 2 * pu) * kKB, k1 = pre ? s.t.pre_keys : s.t.keys;
+            buf ^= 1;
+            const Half f = half_of(a, s, hu);
+            const bool pre = f.pre;
+            const int kb = f.kb, k1 = f.k1;
+            wait_keys();
+            __syncthreads();  // this half is here, the other buffer free
+            if (hu + 1 < 2 * (s.k + s.n)) start_keys<D>(a, s.g, half_of(a, s, hu + 1), sm.k[buf ^ 1], sm.v[buf ^ 1]);
             if (kb >= k1) continue;
-            __syncthreads();
-            load_keys<D>(a, s.g, kb, k1, pre ? pre_list : own_list, sm);
+            const float *kt = sm.k[buf], *vt = sm.v[buf];
             float sc[MR][4];
 #pragma unroll
             for (int i = 0; i < MR; ++i)
@@ -117,17 +322,12 @@ __device__ void run_segment(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
             for (int d = 0; d < D; d += 4) {
                 float4 kx[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) kx[j] = *reinterpret_cast<const float4 *>(sm.k + (tx + 16 * j) * LD + d);
+                for (int j = 0; j < 4; ++j) kx[j] = *reinterpret_cast<const float4 *>(kt + (tx + 16 * j) * LD + d);
 #pragma unroll
                 for (int i = 0; i < MR; ++i) {
-                    const float4 qx = *reinterpret_cast<const float4 *>(sm.q + (ty * MR + i) * LD + d);
+                    const float4 qx = *reinterpret_cast<const float4 *>(sm.q + (ty * MR + i) * LQ + d);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float t = sc[i][j];
-                        t = fmaf(qx.x, kx[j].x, t); t = fmaf(qx.y, kx[j].y, t);
-                        t = fmaf(qx.z, kx[j].z, t); t = fmaf(qx.w, kx[j].w, t);
-                        sc[i][j] = t;
-                    }
+                    for (int j = 0; j < 4; ++j) sc[i][j] = dot4(qx, kx[j], sc[i][j]);
                 }
             }
             bool masked = false;
@@ -158,7 +358,7 @@ __device__ void run_segment(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
                 for (int x = 8; x >= 1; x >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, x);
                 l[i] = l[i] * al + ps;
 #pragma unroll
-                for (int c = 0; c < 4 * NC; ++c) o[i][c] *= al;
+                for (int c = 0; c < NC; ++c) scale4(al, o[i][c]);
             }
             __syncwarp();
             const int kn = min(kKB, k1 - kb);
@@ -170,16 +370,13 @@ __device__ void run_segment(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
                 for (int e = 0; e < 4; ++e) {
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
-                        const float4 vx = *reinterpret_cast<const float4 *>(sm.v + (k + e) * LD + 64 * c + 4 * tx);
+                        const float4 vx = *reinterpret_cast<const float4 *>(vt + (k + e) * LD + 64 * c + 4 * tx);
 #pragma unroll
                         for (int i = 0; i < MR; ++i) {
                             const float p = e == 0 ? px[i].x : e == 1 ? px[i].y : e == 2 ? px[i].z : px[i].w;
                             // a weight of 0 at a key the row does not see must not meet its value
                             if (masked && p == 0.f) continue;
-                            o[i][4 * c] = fmaf(p, vx.x, o[i][4 * c]);
-                            o[i][4 * c + 1] = fmaf(p, vx.y, o[i][4 * c + 1]);
-                            o[i][4 * c + 2] = fmaf(p, vx.z, o[i][4 * c + 2]);
-                            o[i][4 * c + 3] = fmaf(p, vx.w, o[i][4 * c + 3]);
+                            axpy4(p, vx, o[i][c]);
                         }
                     }
                 }
@@ -190,24 +387,9 @@ __device__ void run_segment(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
         for (int i = 0; i < MR; ++i) {
             const int rr = rb + ty * MR + i;
             if (rr >= rows) continue;
-            if (s.direct) {
-                const size_t th = (size_t)(s.t.tok0 + rr / a.G) * a.Hq + s.g * a.G + rr % a.G;
-                const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    float x[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[e] = o[i][4 * c + e] * inv;
-                    store_vec<float, 4>(static_cast<float *>(a.out) + th * D + 64 * c + 4 * tx, x);
-                }
-                if (a.lse && tx == 0) a.lse[th] = l[i] == 0.f ? kNegInf : (m[i] + log2f(l[i])) * kLn2;
-            } else {
-#pragma unroll
-                for (int c = 0; c < NC; ++c)
-                    *reinterpret_cast<float4 *>(a.ws_o + partial_at(s.prow, rows, rr, 64 * c + 4 * tx, D)) =
-                        make_float4(o[i][4 * c], o[i][4 * c + 1], o[i][4 * c + 2], o[i][4 * c + 3]);
-                if (tx == 0) a.ws_ml[s.prow + rr] = make_float2(m[i], l[i]);
-            }
+            for (int c = 0; c < NC; ++c)
+                store_row<D>(a, s, rows, rr, 64 * c + 4 * tx, o[i][c], m[i], l[i], c == 0 && tx == 0);
         }
     }
 }
@@ -227,8 +409,8 @@ shared_attn_kernel(const AttnArgs a) {
     Walk walk(a, h, blockIdx.x);  // one block per worker
     Seg s;
     while (walk.step(s)) {
-        if (s.t.ntok * a.G <= 16) run_segment<D, 1>(a, s, sm);
-        else run_segment<D, 4>(a, s, sm);
+        if (s.t.ntok * a.G <= kFew) run_few<D>(a, s, sm);
+        else run_many<D>(a, s, sm);
     }
 }
 
