@@ -107,7 +107,7 @@ struct AttnArgs {
     const int *prefix_table;  // [NG][max_prefix_pages]
     void *out;                // [T][Hq][d]
     float *lse;               // [T][Hq] or null
-    int R, NG, T, Hq, Hkv, G, d, S, shift, n_pages, max_pages, max_prefix_pages, workers;
+    int R, NG, T, Hq, Hkv, G, gshift, d, S, shift, n_pages, max_pages, max_prefix_pages, workers;
     float sl2;                // softmax scale * log2(e)
     float2 *ws_ml;            // partial (max, sum), base-2 logits
     float *ws_o;              // partial unnormalised outputs

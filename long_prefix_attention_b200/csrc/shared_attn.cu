@@ -646,6 +646,7 @@ cudaError_t asm_shared_attention_launch(const void *q, const void *k_pages, cons
     a.R = R; a.NG = NG; a.T = T; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.d = d;
     a.S = page_size;
     while ((1 << a.shift) < page_size) ++a.shift;
+    while ((1 << a.gshift) < a.G) ++a.gshift;
     a.n_pages = n_pages; a.max_pages = max_pages; a.max_prefix_pages = max_prefix_pages;
     a.workers = workers;
     a.sl2 = scale * kLog2e;

@@ -29,7 +29,8 @@
 // and epilogue run under the other's products.
 // Decode tiles with a few rows waste most of a product, which costs nothing:
 // a 128-key unit takes the tensor core 0.6 us and 64 KB take an SM's share of
-// HBM 1.5 us; warps without rows skip the softmax.
+// HBM 1.5 us.  Up to 32 rows are laid out four times, and each warp of a stream
+// takes a quarter of the keys; above that, warps without rows skip the softmax.
 // Tensor memory columns: O_0 [0,128) O_1 [128,256) S_0 / P_0 [256,384)
 // S_1 / P_1 [384,512).  A stream's products complete in issue order, so S_x(next)
 // (issued after P_x V) overwrites P_x only once it was read, and its completion
@@ -79,7 +80,7 @@ struct __align__(16) SegDesc {
     int g, k, n, pre_keys;           // KV head, first unit, units; as in Tile
     long long prow;                  // first partial row
     int row, masked;                 // row; first unit that some of the tile's rows see in part
-    int direct, pad[3];
+    int direct, group, pad[2];       // group: of the prefix keys
 };
 
 template <int D>
@@ -88,9 +89,11 @@ struct Smem {
     unsigned char kv[Cfg<D>::RING][Cfg<D>::TILE];
     SegDesc seg[kSegs];
     float2 ml[2][128];                 // a row's (max, sum) in each stream
+    float4 wl[8][kSmallRows];          // short tiles: a warp's (factor, share of the sum, maximum) of a row
+    float ex[8][512];                  // short tiles: the warps' outputs on their way to one sum
     uint32_t fix[kFix][kFixUnits][4];  // per segment (modulo kFix): keys whose V was cleared, from the first masked unit on
     uint64_t kv_full[Cfg<D>::RING], kv_empty[Cfg<D>::RING];
-    uint64_t seg_full[kSegs], lag[Cfg<D>::RING / 2], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
+    uint64_t seg_full[kSegs], turn[2][Cfg<D>::RING / 2], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
     uint32_t tmem_base;
 };
 
@@ -140,6 +143,39 @@ __device__ __forceinline__ int units_of(int keys) { return (keys + kUnitKeys - 1
 // not see, since it is a later token; the tile's units if there is none.
 __device__ __forceinline__ int first_masked_unit(const Tile &t) {
     return min(units_of(t.pre_keys) + max(t.base + 1, 0) / kUnitKeys, t.units);
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// The largest of 32 scores; a NaN is the largest.
+__device__ __forceinline__ float max32(const uint32_t (&v)[32]) {
+    float m11[11];
+#pragma unroll
+    for (int i = 0; i < 10; ++i)
+        m11[i] = max3_nan(__uint_as_float(v[3 * i]), __uint_as_float(v[3 * i + 1]), __uint_as_float(v[3 * i + 2]));
+    m11[10] = max_nan(__uint_as_float(v[30]), __uint_as_float(v[31]));
+    return max3_nan(max3_nan(max3_nan(m11[0], m11[1], m11[2]), max3_nan(m11[3], m11[4], m11[5]),
+                             max3_nan(m11[6], m11[7], m11[8])), m11[9], m11[10]);
+}
+
+// A warp's rows of O times f (a lane's own).
+template <int D>
+__device__ __forceinline__ void scale_outputs(uint32_t t_o, float f) {
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t o[32];
+        tmem_ld32(t_o + (uint32_t)c0, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+        tmem_st32(t_o + (uint32_t)c0, o);
+    }
 }
 
 // Scores of places from n on: -inf.
@@ -195,7 +231,10 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
             mbar_init(&sm.kv_empty[i], 2);   // one arrival of each issuer, or two of one
         }
         for (int i = 0; i < kSegs; ++i) mbar_init(&sm.seg_full[i], 1);
-        for (int i = 0; i < RING / 2; ++i) mbar_init(&sm.lag[i], 1);
+        for (int i = 0; i < RING / 2; ++i) {
+            mbar_init(&sm.turn[0][i], 1);
+            mbar_init(&sm.turn[1][i], 1);
+        }
         for (int x = 0; x < 2; ++x) {
             mbar_init(&sm.q_full[x], 1);
             mbar_init(&sm.q_empty[x], 2);
@@ -239,7 +278,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 if (some) {
                     d.tok0 = s.t.tok0; d.rows = s.t.ntok * a.G; d.base = s.t.base; d.keys = s.t.keys;
                     d.g = s.g; d.k = s.k; d.n = s.n; d.pre_keys = s.t.pre_keys;
-                    d.prow = s.prow; d.row = s.t.row; d.masked = first_masked_unit(s.t); d.direct = s.direct;
+                    d.prow = s.prow; d.row = s.t.row; d.group = s.t.group; d.masked = first_masked_unit(s.t); d.direct = s.direct;
                 }
                 sm.seg[segs % kSegs] = d;
                 mbar_arrive(&sm.seg_full[segs % kSegs]);
@@ -265,11 +304,19 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 if (!ok) break;
                 ++qn[x];
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&sm.q_full[x], C::HALVES * 128 * (small ? kSmallRows : kTileRows));
+                    mbar_arrive_expect_tx(&sm.q_full[x], C::TILE);
 #pragma unroll
-                    for (int hf = 0; hf < C::HALVES; ++hf)
-                        tma_load_4d(sm.q[x] + hf * kBox, small ? &maps.q_small : &maps.q, 64 * hf, 0, s.g,
-                                    s.t.tok0 + (dual ? x * tok_x : 0), &sm.q_full[x]);
+                    for (int hf = 0; hf < C::HALVES; ++hf) {
+                        if (small) {   // the same rows in every quarter of the lanes
+#pragma unroll
+                            for (int i = 0; i < kTileRows / kSmallRows; ++i)
+                                tma_load_4d(sm.q[x] + hf * kBox + i * kSmallRows * 128, &maps.q_small, 64 * hf, 0, s.g,
+                                            s.t.tok0, &sm.q_full[x]);
+                        } else {
+                            tma_load_4d(sm.q[x] + hf * kBox, &maps.q, 64 * hf, 0, s.g,
+                                        s.t.tok0 + (dual ? x * tok_x : 0), &sm.q_full[x]);
+                        }
+                    }
                 }
                 __syncwarp();
             }
@@ -331,7 +378,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
             int n = 0, j = 0, dj = 1, qb = 0, next_qb = 0;
             uint32_t segs = 0, step = 0, unit0 = 0;     // before the segment
             uint32_t q_bits = 0;                        // phases of the query buffers
-            uint32_t lag_bits = 0;
+            uint32_t turn_bits = 0;
             bool dual = false;
             auto next = [&]() {      // false behind the last step
                 j += dj;
@@ -358,13 +405,13 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 return true;
             };
             auto issue_s = [&]() {
-                // A tall tile's second stream takes its scores when the first has found its
-                // maximum: left alone, the streams fall into step and the tensor cores
-                // idle during both softmaxes.  (The first can be ahead by the ring's units.)
-                if (dual && x == 1) {
+                // A tall tile's streams take their scores in turns, each when the other has
+                // found its maximum: left alone, they fall into step and the tensor cores
+                // idle during both softmaxes (prompt chunks: 805 against 715 us).
+                if (dual && (x == 1 || j > 0)) {
                     const int i = (unit0 + (uint32_t)j) % (RING / 2);
-                    wait1(&sm.lag[i], (lag_bits >> i) & 1);
-                    lag_bits ^= 1u << i;
+                    wait1(&sm.turn[x][i], (turn_bits >> i) & 1);
+                    turn_bits ^= 1u << i;
                 }
                 if (j < dj) {        // the stream's first step of the segment
                     wait1(&sm.q_full[qb], (q_bits >> qb) & 1);
@@ -420,6 +467,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
         const int x = warp >> 2;            // stream
         const int qd = warp & 3;            // tensor-memory lane quarter
         const int row = qd * 32 + lane;     // row within the stream's 128
+        const int st = tid & 127;           // thread of the stream
         const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
         const uint32_t t_s = tmem + lane_off + 256 + (uint32_t)(x * 128);
         const float sl2 = a.sl2;
@@ -443,13 +491,222 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 continue;
             }
             const bool joint = dual || n > 1;             // both streams have steps
+            const int pre_keys = s.pre_keys, pu = units_of(pre_keys);
+            uint32_t(&fix)[kFixUnits][4] = sm.fix[seg % kFix];
+            const bool fixable = masked < k0 + n;
+            // V of this stream's unit j as the products may use it
+            auto clean = [&](int j) {
+                const int unit = k0 + j, key0 = (unit < pu ? unit : unit - pu) * kUnitKeys;
+                const int valid = (unit < pu ? pre_keys : keys) - key0;
+                if (unit < masked && valid >= kUnitKeys) return;
+                const uint32_t item = item0 + 2 * (uint32_t)j + 1;
+                wait(&sm.kv_full[item % RING], (item / RING) & 1);
+                if (!ok) return;
+                const int r0 = unit >= masked ? max(s.base + 1 - key0, 0) : kUnitKeys;
+                clean_values<D>(sm.kv[item % RING], r0, min(valid, kUnitKeys), row,
+                                fix[min(max(unit - masked, 0), kFixUnits - 1)]);
+            };
+            auto notes = [&]() {       // were values cleared?
+                uint32_t f = 0;
+                for (int fu = 0; fixable && fu < kFixUnits; ++fu) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(fix[fu]);
+                    f |= w.x | w.y | w.z | w.w;
+                }
+                return f;
+            };
+            // the 32 values from column c on that were cleared of keys before `own`: add(i, value)
+            auto add_back = [&](int own, int c, auto add) {
+#pragma unroll 1
+                for (int f = 0; f < kFixUnits * 4; ++f) {
+                    uint32_t bits = fix[f >> 2][f & 3];
+                    while (bits) {
+                        const int key = (masked - pu) * kUnitKeys + 32 * f + __ffs(bits) - 1;
+                        bits &= bits - 1;
+                        if (key >= own) continue;
+                        const int id = a.table[(size_t)s.row * a.max_pages + (key >> a.shift)];
+                        if (id < 0 || id >= a.n_pages) continue;
+                        const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(a.v_pages) +
+                            ((((long long)id * a.Hkv + s.g) << a.shift) + (key & (a.S - 1))) * D + c;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float y = __bfloat162float(vp[i]);
+                            if (!(y - y == 0.f)) add(i, y);
+                        }
+                    }
+                }
+            };
+
+            // o[i]: the sum of the non-finite values, if there are any, of column c + i over
+            // the segment's prefix keys and its local keys before `own`
+            auto sum_non_finite = [&](int own, int c, float (&o)[4]) {
+                const int *pre_list = a.prefix_table + (size_t)s.group * a.max_prefix_pages;
+                const int *own_list = a.table + (size_t)s.row * a.max_pages;
+                float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                for (int u = k0; u < k0 + n; ++u) {
+                    const int key0 = (u < pu ? u : u - pu) * kUnitKeys, end = min(u < pu ? pre_keys : own, key0 + kUnitKeys);
+#pragma unroll 1
+                    for (int key = key0; key < end; ++key) {
+                        const int id = (u < pu ? pre_list : own_list)[key >> a.shift];
+                        if (id < 0 || id >= a.n_pages) continue;
+                        float y[4];
+                        load_vec<__nv_bfloat16, 4>(static_cast<const __nv_bfloat16 *>(a.v_pages) +
+                            ((((long long)id * a.Hkv + s.g) << a.shift) + (key & (a.S - 1))) * D + c, y);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (!(y[i] - y[i] == 0.f)) t[i] += y[i];
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (t[i] != 0.f) o[i] = t[i];   // a NaN is not 0 either
+            };
+
+            if (rows <= kSmallRows) {
+                // ------------------------------------------------ short tile
+                // The tile's rows lie in every quarter of the lanes, and the warp of a
+                // quarter takes 32 of the unit's 128 keys: a softmax of a quarter of
+                // the length, with a state of its own.  The weights of the other
+                // keys are zeros, so its outputs are those of its keys.
+                const bool live = lane < rows;
+                const int own = live ? min(s.base + (lane >> a.gshift) + 1, keys) : keys;   // local keys the row sees
+                float m_used = kNegInf, l = 0.f;
+                for (int j = j0; j < n; j += dj) {
+                    wait(&sm.s_full[x], sn & 1);
+                    ++sn;
+                    tc_fence_after();
+                    const int vis = (k0 + j < pu ? pre_keys - (k0 + j) * kUnitKeys
+                                                 : own - (k0 + j - pu) * kUnitKeys) - 32 * qd;
+                    uint32_t v[32], pk[16];
+                    tmem_ld32(t_s + (uint32_t)(32 * qd), v);
+                    tmem_wait_ld();
+                    if (__any_sync(0xffffffffu, vis < 32)) mask32(v, vis);
+                    const float mt = max32(v) * sl2;
+                    float alpha = 1.f;
+                    if (live && !(mt <= m_used + kRescale)) {
+                        alpha = ex2f(m_used - mt);
+                        m_used = mt;
+                        l *= alpha;
+                    }
+                    const float ref = m_used == kNegInf ? 0.f : m_used;
+                    const uint64_t sl2x2 = pack_f32x2(sl2, sl2), negm2 = pack_f32x2(-ref, -ref);
+                    uint64_t acc[2] = {0, 0};
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint64_t t2 = fma_f32x2(pack_u32x2(v[2 * i], v[2 * i + 1]), sl2x2, negm2);
+                        const uint64_t p2 = pack_f32x2(ex2f(lo_f32(t2)), ex2f(hi_f32(t2)));
+                        acc[i & 1] = add_f32x2(acc[i & 1], p2);
+                        pk[i] = pack_bf16(lo_f32(p2), hi_f32(p2));
+                    }
+                    const uint64_t a01 = add_f32x2(acc[0], acc[1]);
+                    l += lo_f32(a01) + hi_f32(a01);
+                    const uint32_t zero[16] = {0};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (c != qd) tmem_st16(t_s + (uint32_t)(16 * c), zero);
+                    tmem_st16(t_s + (uint32_t)(16 * qd), pk);
+                    if (j > j0 && __any_sync(0xffffffffu, alpha != 1.f)) scale_outputs<D>(tmem + lane_off + (uint32_t)(x * 128), alpha);
+                    tmem_wait_st();
+                    clean(j);
+                    tc_fence_before();
+                    mbar_arrive(&sm.p_full[x]);
+                }
+                // the states of the quarters, of both streams if both have some, become one
+                sm.ml[x][row] = make_float2(m_used, l);
+                wait(&sm.o_full[x], on[x] & 1);
+                if (joint) wait(&sm.o_full[x ^ 1], on[x ^ 1] & 1);
+                ++on[x];
+                if (joint) ++on[x ^ 1];
+                auto meet = [&]() {
+                    if (joint) softmax_sync();
+                    else stream_sync(x);
+                };
+                meet();
+                tc_fence_after();
+                const uint32_t fixed = notes();
+                const int w_lo = joint ? 0 : 4 * x, w_hi = joint ? 8 : 4 * x + 4;   // warps with states
+                // columns per pass, and this thread's row and four columns of a pass
+                int csh = 4;
+                while ((1 << csh) < D && (rows << csh) <= 256) ++csh;
+                const int cols = 1 << csh, it = joint ? tid : st, ir = it >> (csh - 2), ic = (it & (cols / 4 - 1)) * 4;
+                float w_own;
+                {
+                    float ms[8], mo = kNegInf;
+#pragma unroll
+                    for (int w = 0; w < 8; ++w)
+                        ms[w] = w >= w_lo && w < w_hi ? sm.ml[w >> 2][(w & 3) * 32 + lane].x : kNegInf;
+#pragma unroll
+                    for (int w = 0; w < 8; ++w) mo = max_nan(mo, ms[w]);
+                    w_own = ex2f(m_used - (mo == kNegInf ? 0.f : mo));
+                    sm.wl[warp][lane] = make_float4(w_own, w_own * l, mo, 0.f);   // factor, share of the sum, maximum
+                }
+                const int itk = ir >> a.gshift;
+                const size_t th = (size_t)(s.tok0 + itk) * a.Hq + (size_t)s.g * a.G + (ir & (a.G - 1));
+                float mi = kNegInf, li = 0.f, inv = 1.f;
+                for (int c0 = 0; c0 < D; c0 += cols) {
+#pragma unroll 1
+                    for (int c = c0; c < c0 + cols; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(tmem + lane_off + (uint32_t)(x * 128 + c), o);
+                        tmem_wait_ld();
+                        if (live) {
+                            float *e = &sm.ex[warp][(lane << csh) + c - c0];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = w_own == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * w_own);
+#pragma unroll
+                            for (int i = 0; i < 16; i += 4)
+                                *reinterpret_cast<uint4 *>(e + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        }
+                    }
+                    meet();
+                    if (ir < rows) {
+                        if (c0 == 0) {
+#pragma unroll
+                            for (int w = 0; w < 8; ++w)
+                                if (w >= w_lo && w < w_hi) {
+                                    const float4 y = sm.wl[w][ir];
+                                    li += y.y;
+                                    mi = y.z;
+                                }
+                            if (s.direct) inv = li == 0.f ? 0.f : 1.f / li;
+                        }
+                        float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int w = 0; w < 8; ++w)
+                            if (w >= w_lo && w < w_hi) {
+                                const float4 y = *reinterpret_cast<const float4 *>(&sm.ex[w][(ir << csh) + ic]);
+                                o[0] += y.x; o[1] += y.y; o[2] += y.z; o[3] += y.w;
+                            }
+                        // Non-finite values: those cleared, and those that met the zeros of other
+                        // quarters (0 times infinity is not a number).  The sum of the ones
+                        // the row sees is the result; a NaN among the scores is in l already.
+                        const float bad = (o[0] - o[0]) + (o[1] - o[1]) + (o[2] - o[2]) + (o[3] - o[3]);
+                        if ((fixed || bad != 0.f) && li == li) sum_non_finite(min(s.base + itk + 1, keys), c0 + ic, o);
+                        if (s.direct) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) o[i] *= inv;
+                            store_vec<__nv_bfloat16, 4>(static_cast<__nv_bfloat16 *>(a.out) + th * D + c0 + ic, o);
+                        } else {
+                            *reinterpret_cast<float4 *>(a.ws_o + partial_at(s.prow, rows, ir, c0 + ic, D)) =
+                                make_float4(o[0], o[1], o[2], o[3]);
+                        }
+                    }
+                    meet();
+                }
+                if (ir < rows && ic == 0) {
+                    if (!s.direct) a.ws_ml[s.prow + ir] = make_float2(mi, li);
+                    else if (a.lse) a.lse[th] = li == 0.f ? kNegInf : (mi + log2f(li)) * kLn2;
+                }
+                tc_fence_before();
+                if (fixed && it < kFixUnits * 4) fix[it >> 2][it & 3] = 0;
+                continue;
+            }
+
             const int r = dual ? x * 128 + row : row;       // row of the tile
             const bool live = r < rows;
             const bool warp_live = (dual ? x * 128 : 0) + qd * 32 < rows;
-            const int tk = r / a.G;
-            const int pre_keys = s.pre_keys, pu = units_of(pre_keys);
+            const int tk = r >> a.gshift;
             const int own = live ? min(s.base + tk + 1, keys) : keys;   // local keys the row sees
-            uint32_t(&fix)[kFixUnits][4] = sm.fix[seg % kFix];
             float m_used = kNegInf, l = 0.f;
             for (int j = j0; j < n; j += dj) {
                 wait(&sm.s_full[x], sn & 1);
@@ -467,14 +724,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                         tmem_ld32(t_s + (uint32_t)(32 * c), v);
                         tmem_wait_ld();
                         if (part) mask32(v, vis - 32 * c);
-                        float m11[11];
-#pragma unroll
-                        for (int i = 0; i < 10; ++i)
-                            m11[i] = max3_nan(__uint_as_float(v[3 * i]), __uint_as_float(v[3 * i + 1]),
-                                              __uint_as_float(v[3 * i + 2]));
-                        m11[10] = max_nan(__uint_as_float(v[30]), __uint_as_float(v[31]));
-                        mraw = max3_nan(mraw, max3_nan(max3_nan(m11[0], m11[1], m11[2]), max3_nan(m11[3], m11[4], m11[5]),
-                                                       max3_nan(m11[6], m11[7], m11[8])), max_nan(m11[9], m11[10]));
+                        mraw = max_nan(mraw, max32(v));
                     }
                     const float mt = mraw * sl2;
                     float alpha = 1.f;
@@ -484,18 +734,8 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                         l *= alpha;
                     }
                     // tensor-memory access is warp-wide: rows that keep their maximum scale by 1
-                    if (j > j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                        const uint32_t t_o = tmem + lane_off + (uint32_t)(x * 128);
-#pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(t_o + (uint32_t)c0, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                            tmem_st32(t_o + (uint32_t)c0, o);
-                        }
-                    }
+                    if (j > j0 && __any_sync(0xffffffffu, alpha != 1.f))
+                        scale_outputs<D>(tmem + lane_off + (uint32_t)(x * 128), alpha);
                     // pass 2: p = 2^(s scale log2(e) - m), rounded to bf16 for the product
                     // with V (the sum keeps fp32); P goes over columns of S already read
                     const float ref = m_used == kNegInf ? 0.f : m_used;
@@ -503,7 +743,8 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                     uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
-                        if (c == 0 && dual && tid == 0) mbar_arrive(&sm.lag[(item0 / 2 + (uint32_t)j) % (RING / 2)]);
+                        if (c == 0 && dual && st == 0 && (x == 0 || j + 1 < n))
+                            mbar_arrive(&sm.turn[x ^ 1][(item0 / 2 + (uint32_t)(j + x)) % (RING / 2)]);
                         uint32_t v[32], pk[16];
                         tmem_ld32(t_s + (uint32_t)(32 * c), v);
                         tmem_wait_ld();
@@ -533,23 +774,11 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                     l += lo_f32(a01) + hi_f32(a01);
                     tmem_wait_st();
                 }
-                const int unit = k0 + j, key0 = (unit < pu ? unit : unit - pu) * kUnitKeys;
-                const int valid = (unit < pu ? pre_keys : keys) - key0;
-                if (unit >= masked || valid < kUnitKeys) {
-                    // V as the product may use it (both streams of a tall tile do the same)
-                    const uint32_t item = item0 + 2 * (uint32_t)j + 1;
-                    wait(&sm.kv_full[item % RING], (item / RING) & 1);
-                    if (ok) {
-                        unsigned char *vt = sm.kv[item % RING];
-                        const int r0 = unit >= masked ? max(s.base + 1 - key0, 0) : kUnitKeys;
-                        clean_values<D>(vt, r0, min(valid, kUnitKeys), row, fix[min(max(unit - masked, 0), kFixUnits - 1)]);
-                    }
-                }
+                clean(j);
                 tc_fence_before();
                 mbar_arrive(&sm.p_full[x]);
             }
             // ------------------------------------------------------ epilogue
-            const bool fixable = masked < k0 + n;
             if (joint) {
                 sm.ml[x][row] = make_float2(m_used, l);
                 wait(&sm.o_full[0], on[0] & 1);
@@ -563,13 +792,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 if (fixable) stream_sync(x);
             }
             tc_fence_after();
-            uint32_t fixed = 0;
-            if (fixable) {
-                for (int fu = 0; fu < kFixUnits; ++fu) {
-                    const uint4 f = *reinterpret_cast<const uint4 *>(fix[fu]);
-                    fixed |= f.x | f.y | f.z | f.w;
-                }
-            }
+            const uint32_t fixed = notes();
             if (warp_live) {
                 // the states of a small tile's streams, joined
                 float w0 = 1.f, w1 = 0.f, m = m_used;
@@ -582,7 +805,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                     w1 = ex2f(s1.x - ref);
                     l = w0 * s0.y + w1 * s1.y;
                 }
-                const size_t th = (size_t)(s.tok0 + tk) * a.Hq + (size_t)s.g * a.G + (r - tk * a.G);
+                const size_t th = (size_t)(s.tok0 + tk) * a.Hq + (size_t)s.g * a.G + (r & (a.G - 1));
                 const float inv = s.direct ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
                 // of two streams, each writes half of the columns
                 const int c_lo = two ? x * (D / 2) : 0, c_hi = two ? c_lo + D / 2 : D;
@@ -604,27 +827,11 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                     } else {
                         tmem_wait_ld();
                     }
-                    if (fixed && live) {
-                        // non-finite values of keys that only some rows see: back into the rows that do
-#pragma unroll 1
-                        for (int f = 0; f < kFixUnits * 4; ++f) {
-                            uint32_t bits = fix[f >> 2][f & 3];
-                            while (bits) {
-                                const int key = (masked - pu) * kUnitKeys + 32 * f + __ffs(bits) - 1;
-                                bits &= bits - 1;
-                                if (key >= own) continue;
-                                const int id = a.table[(size_t)s.row * a.max_pages + (key >> a.shift)];
-                                if (id < 0 || id >= a.n_pages) continue;
-                                const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(a.v_pages) +
-                                    ((((long long)id * a.Hkv + s.g) << a.shift) + (key & (a.S - 1))) * D + c0;
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) {
-                                    const float y = __bfloat162float(vp[i]);
-                                    if (!(y - y == 0.f)) o[i] = __float_as_uint(__uint_as_float(o[i]) + y);
-                                }
-                            }
-                        }
-                    }
+                    // non-finite values of keys that only some rows see: back into the rows that do
+                    if (fixed && live)
+                        add_back(own, c0, [&](int i, float y) {
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) + y);
+                        });
                     if (live) {
                         if (s.direct) {
                             __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + th * D + c0;

@@ -394,6 +394,26 @@ def test_shared_attention_special_values():
         assert torch.isfinite(o).all() and torch.isfinite(lse).all()
 
 
+@pytest.mark.parametrize("rows_per", [1, 3, 20, 40])
+def test_infinite_values_stay_infinite(rows_per):
+    """An infinite value anywhere in the keys a row sees (prefix or local) gives
+    an infinite result in its column; one that it does not see gives nothing."""
+    for dt in ("f32", "bf16"):
+        b = Batch(dt, 4, 2, 64, 32, new=[rows_per] * 2, seq=[150 + rows_per] * 2, goff=[0, 2], pre=[200], seed=17)
+        b.vd[int(b.ptable[0, 3]), 0, 7, 9] = -math.inf          # prefix key 103
+        b.vd[int(b.table[0, 2]), 1, 1, 11] = math.inf           # local key 65 of row 0
+        last = 149 + rows_per
+        b.vd[int(b.table[1, last // 32]), 0, last % 32, 13] = math.inf   # the last new token of row 1
+        out, lse = b.run()
+        o, n = out.cpu(), rows_per
+        assert torch.isfinite(lse).all()
+        assert (o[:, :2, 9] == -math.inf).all()
+        assert (o[:n, 2:, 11] == math.inf).all()
+        assert (o[2 * n - 1, :2, 13] == math.inf).all()
+        o[:, :2, 9], o[:n, 2:, 11], o[2 * n - 1, :2, 13] = 0, 0, 0
+        assert torch.isfinite(o).all()
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_a_later_token_never_reaches_an_earlier_one(dt):
     """Non-finite keys and values of a row's own later tokens stay out of the
