@@ -17,7 +17,9 @@
 // Bound by memory: one read and one write of every element.  A thread keeps
 // one unit of every head (two 16-byte vectors that hold whole pairs), so the
 // sines of a token are formed once per unit and used for all the heads of its
-// slice; neighbouring threads read neighbouring vectors.
+// slice; neighbouring threads read neighbouring vectors, four heads of them in
+// flight (8191 tokens of 32 + 2 x 8 heads appended: 38 us, 81% of the measured
+// copy rate; one head in flight 46, eight 56, which need too many registers).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -28,6 +30,7 @@ namespace asmk {
 namespace rope {
 
 constexpr int kThreads = 256;
+constexpr int kBatch = 4;  // heads in flight per thread
 
 struct View {
     void *p;
@@ -154,13 +157,25 @@ rope_vec_kernel(const Args a, int units, int slices) {
         if (turn || !a.same) {
             const T *x = static_cast<const T *>(a.x.p) + t * a.x.st;
             T *y = static_cast<T *>(a.y.p) + t * a.y.st;
-#pragma unroll 4
-            for (int h = s; h < a.H; h += slices) {
-                uint4 v0 = *reinterpret_cast<const uint4 *>(x + h * a.x.sh + o0);
-                uint4 v1 = *reinterpret_cast<const uint4 *>(x + h * a.x.sh + o1);
-                if (turn) rotate(v0, v1);
-                *reinterpret_cast<uint4 *>(y + h * a.y.sh + o0) = v0;
-                *reinterpret_cast<uint4 *>(y + h * a.y.sh + o1) = v1;
+            // kBatch heads' vectors are read before any is written: x and y may be the
+            // same, so the compiler would not read ahead of a store
+            for (int h0 = s; h0 < a.H; h0 += kBatch * slices) {
+                uint4 v[kBatch][2];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int h = h0 + i * slices;
+                    if (h >= a.H) break;
+                    v[i][0] = *reinterpret_cast<const uint4 *>(x + h * a.x.sh + o0);
+                    v[i][1] = *reinterpret_cast<const uint4 *>(x + h * a.x.sh + o1);
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int h = h0 + i * slices;
+                    if (h >= a.H) break;
+                    if (turn) rotate(v[i][0], v[i][1]);
+                    *reinterpret_cast<uint4 *>(y + h * a.y.sh + o0) = v[i][0];
+                    *reinterpret_cast<uint4 *>(y + h * a.y.sh + o1) = v[i][1];
+                }
             }
         }
         if (APPEND) {

@@ -244,6 +244,10 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
         }
         fence_mbar_init();
     }
+    if (tid >= 32 && tid < 36) {   // the tensor maps' first use should not wait for them
+        const CUtensorMap *m = tid == 32 ? &maps.k : tid == 33 ? &maps.v : tid == 34 ? &maps.q : &maps.q_small;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+    }
     if (tid < kFix * kFixUnits * 4) (&sm.fix[0][0][0])[tid] = 0;
     if (warp == kIssuer) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
