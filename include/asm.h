@@ -615,7 +615,7 @@ asm_status asm_rope_append(const void *q, int64_t q_st, int64_t q_sh,
  * lengths beyond T, R, the tables' pages are clamped.
  *   plan       asm_shared_plan_size(R, NG, T, Hq, Hkv) bytes (any content)
  * NG <= 4096, T <= 2^24.  The plan belongs to these sizes and to the device it
- * was made on.  One launch.
+ * was made on; any number of calls may read it.  One launch.
  */
 size_t asm_shared_plan_size(int R, int NG, int T, int Hq, int Hkv);
 asm_status asm_shared_plan(const int32_t *q_off, const int32_t *seq_len,
@@ -629,23 +629,29 @@ asm_status asm_shared_plan(const int32_t *q_off, const int32_t *seq_len,
  * of their row's group and over the row's own tokens up to themselves: the new
  * token i of n of row r sees the whole prefix and the local keys
  * 0 .. seq_len[r] - n + i.  A prefix is read once for all the rows that share
- * it (per 256 query rows), in contrast to asm_flash_decode for any number of
- * prefixes, new tokens per row and pages.
- *   q, out       [T, Hq, d] dt
+ * it (per 256 query rows of a KV head), in contrast to asm_flash_decode for
+ * any number of prefixes, new tokens per row and pages.
+ *   q, out       [T, Hq, d] dt (out must not overlap q)
  *   k_pages, v_pages [n_pages, Hkv, S, d] dt (the new tokens' included)
  *   table        [R, max_pages] int32, prefix_table [NG, max_prefix_pages]
  *   lse_out      [T, Hq] fp32 (natural log), or NULL
  *   plan         of asm_shared_plan with the same sizes
  *   scale        > 0 and finite
  *   ws           asm_shared_attention_workspace_size(...) bytes, word 0 zeroed
- *                once (asm_workspace_init); asm_workspace_error reads it
+ *                once (asm_workspace_init); asm_workspace_error reads it.  It
+ *                grows with T x Hq (partial states of the rows)
  * A token without any key gets (0, -inf).  Tokens outside every row are left
- * as they were.  Keys behind a row's length are not used, whatever their
- * pages hold.  A page id outside [0, n_pages) reads as zeros and sets the error
- * word to ASM_ERR_INVALID_ARG, and so does a plan of other sizes, with which
- * the call writes nothing.  (out, lse_out) is an attention state: with
- * asm_decode_step over no local tokens and asm_merge_states it joins the
+ * as they were.  Keys that a token does not see (later tokens, places behind a
+ * row's length) never reach its result, whatever their pages hold, infinities
+ * and NaN among it.  A page id outside [0, n_pages) reads as zeros and sets the
+ * error word to ASM_ERR_INVALID_ARG, and so does a plan of other sizes, with
+ * which the call writes nothing; a device-side wait that gives up sets
+ * ASM_ERR_TIMEOUT (outputs not valid).  (out, lse_out) is an attention state:
+ * with asm_decode_step over no local tokens and asm_merge_states it joins the
  * memory's retrieved state in place of an explicit prefix.
+ * bf16 runs on the tcgen05 tensor cores (bf16 products and weights, fp32
+ * accumulators, statistics and joins), fp32 on CUDA cores.  Two launches, with
+ * programmatic dependent launch; equal calls give equal bits.
  */
 size_t asm_shared_attention_workspace_size(int T, int Hq, int Hkv, int d);
 asm_status asm_shared_attention(const void *q, const void *k_pages,

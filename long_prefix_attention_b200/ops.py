@@ -386,7 +386,7 @@ def asm_page_step(kv_len, new_len, pool, pool_state, page_size: int, table, seq_
           q_off.numel() == R + 1 and pos.numel() == T and slot.numel() == T and pool_state.numel() == 3 and
           pool_out.numel() == 3 and (pos_base is None or pos_base.numel() == R))
     _check(fn, _lib.load().asm_page_step(
-        kv_len.data_ptr(), new_len.data_ptr(), _ptr(pos_base), R, page_size, table.shape[1], table.data_ptr(),
+        kv_len.data_ptr(), new_len.data_ptr(), _ptr(pos_base), R, int(page_size), table.shape[1], table.data_ptr(),
         pool.data_ptr(), pool_state.data_ptr(), pool.numel(), T, seq_len.data_ptr(), q_off.data_ptr(), row.data_ptr(),
         pos.data_ptr(), slot.data_ptr(), pool_out.data_ptr(), _raw_stream(dev, stream)))
 
@@ -398,7 +398,8 @@ def asm_rope_freqs(freq, theta: float, scaling: int = ASM_ROPE_SCALE_NONE, facto
     dev = _take(fn, (freq,))
     _f64(fn, freq)
     _check(fn, _lib.load().asm_rope_freqs(
-        freq.data_ptr(), 2 * freq.numel(), theta, scaling, factor, lo, hi, ctx, _raw_stream(dev, stream)))
+        freq.data_ptr(), 2 * freq.numel(), float(theta), int(scaling), float(factor), float(lo), float(hi), float(ctx),
+        _raw_stream(dev, stream)))
 
 
 def asm_rope(x, pos, freq, y, layout: int = ASM_ROPE_HALF, mscale: float = 1.0, inverse: bool = False, stream=None):
@@ -413,8 +414,8 @@ def asm_rope(x, pos, freq, y, layout: int = ASM_ROPE_HALF, mscale: float = 1.0, 
     _want(fn, y.shape == x.shape and pos.numel() == T)
     xs, ys = _heads(fn, x, T, d, x.dtype), _heads(fn, y, T, d, x.dtype)
     _check(fn, _lib.load().asm_rope(
-        x.data_ptr(), *xs, T, H, d, _dt(x), pos.data_ptr(), freq.data_ptr(), 2 * freq.numel(), layout, mscale,
-        1 if inverse else 0, y.data_ptr(), *ys, _raw_stream(dev, stream)))
+        x.data_ptr(), *xs, T, H, d, _dt(x), pos.data_ptr(), freq.data_ptr(), 2 * freq.numel(), int(layout),
+        float(mscale), 1 if inverse else 0, y.data_ptr(), *ys, _raw_stream(dev, stream)))
 
 
 def asm_rope_append(q, k, v, pos, slot, freq, q_out, k_pages, v_pages, layout: int = ASM_ROPE_HALF,
@@ -436,7 +437,7 @@ def asm_rope_append(q, k, v, pos, slot, freq, q_out, k_pages, v_pages, layout: i
     qs, ks, vs, os = _heads(fn, q, T, d, dt), _heads(fn, k, T, d, dt), _heads(fn, v, T, d, dt), _heads(fn, q_out, T, d, dt)
     _check(fn, _lib.load().asm_rope_append(
         q.data_ptr(), *qs, k.data_ptr(), *ks, v.data_ptr(), *vs, T, Hq, Hkv, d, _dt(q), pos.data_ptr(), slot.data_ptr(),
-        freq.data_ptr(), 2 * freq.numel(), layout, mscale, q_out.data_ptr(), *os, k_pages.data_ptr(),
+        freq.data_ptr(), 2 * freq.numel(), int(layout), float(mscale), q_out.data_ptr(), *os, k_pages.data_ptr(),
         v_pages.data_ptr(), pages[0], pages[2], _raw_stream(dev, stream)))
 
 
@@ -458,8 +459,8 @@ def asm_shared_plan(q_off, seq_len, table, T: int, Hq: int, Hkv: int, page_size:
     _want(fn, NG <= 0 or (prefix_len is not None and prefix_table is not None and prefix_len.numel() == NG and
                           prefix_table.dim() == 2 and prefix_table.shape[0] == NG))
     _check(fn, _lib.load().asm_shared_plan(
-        q_off.data_ptr(), seq_len.data_ptr(), _ptr(group_off), _ptr(prefix_len), R, NG, T, Hq, Hkv, page_size,
-        table.shape[1], prefix_table.shape[1] if NG > 0 else 0, plan.data_ptr(), plan.numel() * plan.element_size(),
+        q_off.data_ptr(), seq_len.data_ptr(), _ptr(group_off), _ptr(prefix_len), R, NG, int(T), int(Hq),
+        int(Hkv), int(page_size), table.shape[1], prefix_table.shape[1] if NG > 0 else 0, plan.data_ptr(), plan.numel() * plan.element_size(),
         _raw_stream(dev, stream)))
 
 
@@ -484,7 +485,7 @@ def asm_shared_attention(q, k_pages, v_pages, table, plan, scale: float, out, ws
     _check(fn, _lib.load().asm_shared_attention(
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), pages[0], pages[2], table.data_ptr(), table.shape[1],
         _ptr(prefix_table), prefix_table.shape[1] if NG else 0, plan.data_ptr(), plan.numel() * plan.element_size(),
-        table.shape[0], NG, T, Hq, pages[1], d, scale, _dt(q), out.data_ptr(), _ptr(lse_out), ws.data_ptr(),
+        table.shape[0], NG, T, Hq, pages[1], d, float(scale), _dt(q), out.data_ptr(), _ptr(lse_out), ws.data_ptr(),
         ws.numel() * ws.element_size(), _raw_stream(dev, stream)))
 
 

@@ -364,6 +364,19 @@ def test_shared_attention_mixes_segments(dt, Hq, Hkv):
     Batch(dt, Hq, Hkv, 64, 32, new=new, seq=seq, goff=[4, 30, 33, 80], pre=[400, 90, 129], seed=13).check()
 
 
+def test_shared_attention_most_rows_and_groups():
+    """4096 rows in 900 groups, some empty, some with tall rows between short ones."""
+    rng = random.Random(3)
+    new = [1] * 4096
+    for r in (5, 700, 701, 2000):
+        new[r] = 70
+    new[9] = 0
+    seq = [n + rng.randint(0, 6) for n in new]
+    cuts = sorted(rng.randint(0, 4096) for _ in range(901))
+    pre = [rng.randint(0, 20) for _ in range(900)]
+    Batch("bf16", 2, 1, 64, 16, new=new, seq=seq, goff=cuts, pre=pre, seed=14).check()
+
+
 def test_shared_attention_large_logits():
     """Scores of some hundreds: the running maximum moves far, weights underflow."""
     for dt in ("bf16", "f32"):

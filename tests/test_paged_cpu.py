@@ -146,46 +146,89 @@ def test_binding_refuses_host_tensors_and_other_types():
         ops._i32("f", i.long())
 
 
+def plan_tiles(new, old, pre, cuts, G):
+    """The tiles of a plan, (query rows per KV head, units) each, as the plan
+    kernel lays them out: prefix tiles over the runs of rows of up to 128 query
+    rows, then every row's own, which hold the prefix too where the row has
+    more."""
+    single, dual = 128 // G, 256 // G
+
+    def split(n):
+        return [] if n <= 0 else [n] if n <= single else [min(dual, n - i) for i in range(0, n, dual)]
+
+    group = [next((g for g in range(len(pre)) if cuts[g] <= r < cuts[g + 1]), None) for r in range(len(new))]
+    tiles, run, at = [], 0, None
+    runs = []
+    for r, g in enumerate(group):
+        if g is None or new[r] > single:
+            at = None
+            continue
+        if at != g:
+            runs.append([g, 0])
+            at = g
+        runs[-1][1] += new[r]
+    for g, n in runs:
+        tiles += [(t * G, C.cdiv(pre[g], 128)) for t in split(n)]
+    for r, n in enumerate(new):
+        done = 0
+        for t in split(n):
+            done += t
+            both = C.cdiv(pre[group[r]], 128) if n > single and group[r] is not None else 0
+            tiles.append((t * G, both + C.cdiv(old[r] + done, 128)))
+    return tiles
+
+
 @pytest.mark.parametrize("G", [1, 2, 4, 8])
-def test_partial_rows_and_tiles_stay_within_their_bounds(lib, G):
-    """The plan's tile count and the partial rows it hands out, computed here
-    for random lengths, never exceed what the size functions provide for."""
+def test_the_plans_bounds_hold(lib, G):
+    """For random lengths: the tiles, the partial rows and the segments never
+    exceed what the size functions provide for, and the workers' ranges take
+    every unit once."""
     import random
     rng = random.Random(G)
     Hkv, workers = 4, 148
     Hq = G * Hkv
-    single, dual = 128 // G, 256 // G
-
-    def tiles(n):
-        return [] if n <= 0 else [n] if n <= single else [min(dual, n - i) for i in range(0, n, dual)]
-
-    for _ in range(200):
+    unit_cost = lambda rows: 4 if rows > 128 else 2          # noqa: E731
+    head_cost = lambda rows: 4 if rows > 128 else 3          # noqa: E731
+    for _ in range(150):
         R, NG = rng.randint(1, 60), rng.randint(0, 4)
         new = [rng.choice([0, 1, 1, 3, rng.randint(0, 900)]) for _ in range(R)]
-        T = max(1, sum(new))
+        old = [rng.choice([0, 100, 9000]) for _ in range(R)]
+        pre = [rng.choice([0, 1, 300, 40000]) for _ in range(NG)]
         cuts = sorted(rng.randint(0, R) for _ in range(NG + 1))
-        off = [0]
-        for n in new:
-            off.append(off[-1] + n)
-        lst = []
-        for g in range(NG):
-            pre = rng.choice([0, 1, 300, 40000])
-            lst += [(n, C.cdiv(pre, 128)) for n in tiles(off[cuts[g + 1]] - off[cuts[g]])]
-        for r in range(R):
-            old, done = rng.choice([0, 100, 9000]), 0
-            for n in tiles(new[r]):
-                done += n
-                lst.append((n, C.cdiv(old + done, 128)))
-        bound = min(R, T) + min(NG, T) + 2 * C.cdiv(T * G, 256)
-        assert len(lst) <= bound
-        W = Hkv * sum(u for _, u in lst)
-        upc = max(1, C.cdiv(W, workers))
-        rows = sum((u // upc + 2) * Hkv * n * G for n, u in lst if u)
-        assert rows <= 4 * T * Hq + (workers + 1) * 256
-        # segments of a pair never exceed its capacity
+        T = max(1, sum(new))
+        tiles = plan_tiles(new, old, pre, cuts, G)
+        assert len(tiles) <= min(R, T) + min(NG, T) + 4 * C.cdiv(T * G, 256)
+        cost = [head_cost(r) + unit_cost(r) * u if u else 0 for r, u in tiles]
+        W = Hkv * sum(cost)
+        size = max(C.cdiv(W, workers), 4 if any(r > 128 for r, _ in tiles) else 2)
+        assert sum((c // size + 2) * Hkv * r for (r, u), c in zip(tiles, cost) if u) <= \
+            4 * T * Hq + (workers + 1) * 256
         c0 = 0
-        for n, u in lst:
+        for (r, u), c in zip(tiles, cost):
             for _ in range(Hkv):
-                if u:
-                    assert (c0 + u - 1) // upc - c0 // upc + 1 <= u // upc + 2
-                c0 += u
+                who = [(c0 + head_cost(r) + unit_cost(r) * k) // size for k in range(u)]
+                if who:
+                    assert who[-1] < workers and who[-1] - who[0] + 1 <= c // size + 2
+                    # no worker between the first and the last goes without a unit
+                    assert sorted(set(who)) == list(range(who[0], who[-1] + 1))
+                c0 += c
+
+
+def test_the_quintic_exponential():
+    """A quarter of the softmax exponentials runs on the FMA pipe
+    (csrc/shared_attn_tc.cu, exp2_poly_x2): the same steps in fp32, a fused
+    multiply-add as an exact product and one rounding, stay within the 2^-20
+    the attention bounds count."""
+    import numpy as np
+    f32 = np.float32
+    co = [f32(x) for x in (0.001327647245, 0.009675540961, 0.05550713092, 0.2402212024, 0.693146944, 1.000000119)]
+    t = np.linspace(-100.0, 20.0, 600_001).astype(f32)
+    y = (t + f32(12582912.0)).astype(f32)
+    n = (y - f32(12582912.0)).astype(f32)
+    fr = (t.astype(np.float64) - n.astype(np.float64)).astype(f32)
+    p = np.full_like(fr, co[0])
+    for c in co[1:]:
+        p = (p.astype(np.float64) * fr.astype(np.float64) + float(c)).astype(f32)
+    bits = (p.view(np.uint32) + (y.view(np.uint32) << np.uint32(23))).astype(np.uint32)
+    got, ref = bits.view(f32).astype(np.float64), np.exp2(t.astype(np.float64))
+    assert (np.abs(got - ref) / ref).max() < 2.0 ** -20 / 2
