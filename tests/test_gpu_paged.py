@@ -364,6 +364,18 @@ def test_shared_attention_mixes_segments(dt, Hq, Hkv):
     Batch(dt, Hq, Hkv, 64, 32, new=new, seq=seq, goff=[4, 30, 33, 80], pre=[400, 90, 129], seed=13).check()
 
 
+@pytest.mark.parametrize("d,S", [(64, 32), (128, 64)])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (8, 2)])
+@pytest.mark.parametrize("n", [31, 32, 33, 47, 63, 64, 65, 96, 97])
+def test_shared_attention_tile_heights(n, Hq, Hkv, d, S):
+    """Query rows per tile around the limits of 32, 64 and 96, split over
+    workers and not: rows of a group, and tokens of one row."""
+    tok = C.cdiv(n, Hq // Hkv)
+    Batch("bf16", Hq, Hkv, d, S, new=[1] * tok, seq=[3 + 2 * i for i in range(tok)], goff=[0, tok], pre=[3000], seed=n).check()
+    Batch("bf16", Hq, Hkv, d, S, new=[tok, tok], seq=[tok + 100, tok], goff=[0, 2], pre=[70], seed=n, pad=1).check()
+    Batch("bf16", Hq, Hkv, d, S, new=[tok], seq=[1500 + tok], seed=n).check()
+
+
 def test_shared_attention_most_rows_and_groups():
     """4096 rows in 900 groups, some empty, some with tall rows between short ones."""
     rng = random.Random(3)
@@ -482,6 +494,21 @@ def test_plan_survives_falling_offsets():
                                  prefix_table=b.dev["prefix_table"])
         torch.cuda.synchronize()
         ops.asm_workspace_error(ws)
+
+
+@pytest.mark.parametrize("tok", [8, 9, 12, 16, 17])
+def test_a_later_token_never_reaches_an_earlier_draft(tok):
+    """As above, for tiles of 32 to 68 query rows, the bad key in either half of a unit."""
+    for seq, bad in ((tok + 60, tok + 55), (tok + 120, tok + 125 - 10)):
+        b = Batch("bf16", 4, 1, 64, 32, new=[tok], seq=[seq], goff=[0, 1], pre=[40], seed=tok)
+        o0, z0 = b.run()
+        pg, at, first = int(b.table[0, bad // 32]), bad % 32, max(bad - (seq - tok), 0)
+        b.vd[pg, :, at, ::3] = math.nan
+        b.vd[pg, :, at, 1::3] = math.inf
+        b.kd[pg, :, at, ::2] = math.nan
+        o1, z1 = b.run()
+        assert torch.equal(o0[:first], o1[:first]) and torch.equal(z0[:first], z1[:first])
+        assert torch.isnan(o1[first:, :, 0]).all() and torch.isnan(z1[first:]).all()
 
 
 def test_shared_attention_repeats_bit_for_bit():

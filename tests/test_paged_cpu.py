@@ -188,7 +188,7 @@ def test_the_plans_bounds_hold(lib, G):
     Hkv, workers = 4, 148
     Hq = G * Hkv
     unit_cost = lambda rows: 4 if rows > 128 else 2          # noqa: E731
-    head_cost = lambda rows: 4 if rows > 128 else 3          # noqa: E731
+    head_cost = lambda rows: 4 if rows > 128 else 2          # noqa: E731
     for _ in range(150):
         R, NG = rng.randint(1, 60), rng.randint(0, 4)
         new = [rng.choice([0, 1, 1, 3, rng.randint(0, 900)]) for _ in range(R)]
