@@ -27,10 +27,14 @@
 // state in both streams, which its epilogue joins.  A stream's next scores are
 // issued right behind its P V, across segments too, so one stream's softmax
 // and epilogue run under the other's products.
-// Decode tiles with a few rows waste most of a product, which costs nothing:
+// Decode tiles with a few rows waste most of a product, which costs no time:
 // a 128-key unit takes the tensor core 0.6 us and 64 KB take an SM's share of
-// HBM 1.5 us.  Up to 32 rows are laid out four times, and each warp of a stream
-// takes a quarter of the keys; above that, warps without rows skip the softmax.
+// HBM 1.5 us.  It does cost power: 64 rows behind 32768 keys, call after call,
+// run at the power limit.  Up to 32 rows are laid out four times, each warp of a
+// stream takes a quarter of the keys, and the rows between them are zeros in Q
+// and in P (64 rows: 357 us at first and 432 for many calls, with the rows that
+// follow in memory 384 and 460).  Above that, warps without rows skip the softmax;
+// 33 to 64 rows laid out twice gained 2% there but cost the shorter tiles 14%.
 // Tensor memory columns: O_0 [0,128) O_1 [128,256) S_0 / P_0 [256,384)
 // S_1 / P_1 [384,512).  A stream's products complete in issue order, so S_x(next)
 // (issued after P_x V) overwrites P_x only once it was read, and its completion
@@ -61,7 +65,9 @@ constexpr float kRescale = 8.f;
 constexpr int kBox = 128 * 128;     // 128 rows x 64 columns of bf16
 constexpr int kFixUnits = 4;        // units of a tile that some of its rows see in part
 constexpr int kFix = 8;             // one stream is at most RING / 2 + 1 segments ahead of the other
-constexpr int kSmallRows = 32;      // query rows of the small box
+constexpr int kSmallRows = 32;      // query rows of a short tile
+constexpr int kBoxRows = 8;         // query rows of its boxes: a swizzle atom, at least one token
+constexpr int kQuarterBoxes = kSmallRows / kBoxRows;
 
 template <int D>
 struct Cfg {
@@ -296,6 +302,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
         uint32_t n = 0;            // ring items so far
         uint32_t qn[2] = {0, 0};   // fills of the query buffers
         int qb = 0;                // buffer of the next small tile
+        int dirty[2] = {kQuarterBoxes, kQuarterBoxes};   // boxes of a quarter that may hold other than zeros
         while (ok && some) {
             s = ns;
             some = walk.step(ns);
@@ -307,20 +314,26 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 if (qn[x] > 0) wait(&sm.q_empty[x], (qn[x] - 1) & 1);
                 if (!ok) break;
                 ++qn[x];
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&sm.q_full[x], C::TILE);
+                // a short tile: the same boxes in every quarter of the lanes, then zeros over
+                // what earlier tiles left (a load from behind the last token gives zeros)
+                const int live = small ? (qrows + kBoxRows - 1) / kBoxRows : kQuarterBoxes;
+                const int loads = max(live, dirty[x]);
+                dirty[x] = live;
+                if (lane == 0) mbar_arrive_expect_tx(&sm.q_full[x], (uint32_t)(small ? C::TILE / kQuarterBoxes * loads : C::TILE));
+                __syncwarp();
+                if (small) {
+                    const int b = lane % kQuarterBoxes;
+                    if (lane < kTileRows / kBoxRows && b < loads) {
 #pragma unroll
-                    for (int hf = 0; hf < C::HALVES; ++hf) {
-                        if (small) {   // the same rows in every quarter of the lanes
-#pragma unroll
-                            for (int i = 0; i < kTileRows / kSmallRows; ++i)
-                                tma_load_4d(sm.q[x] + hf * kBox + i * kSmallRows * 128, &maps.q_small, 64 * hf, 0, s.g,
-                                            s.t.tok0, &sm.q_full[x]);
-                        } else {
-                            tma_load_4d(sm.q[x] + hf * kBox, &maps.q, 64 * hf, 0, s.g,
-                                        s.t.tok0 + (dual ? x * tok_x : 0), &sm.q_full[x]);
-                        }
+                        for (int hf = 0; hf < C::HALVES; ++hf)
+                            tma_load_4d(sm.q[x] + hf * kBox + lane * kBoxRows * 128, &maps.q_small, 64 * hf, 0, s.g,
+                                        b < live ? s.t.tok0 + b * (kBoxRows / a.G) : a.T, &sm.q_full[x]);
                     }
+                } else if (lane == 0) {
+#pragma unroll
+                    for (int hf = 0; hf < C::HALVES; ++hf)
+                        tma_load_4d(sm.q[x] + hf * kBox, &maps.q, 64 * hf, 0, s.g,
+                                    s.t.tok0 + (dual ? x * tok_x : 0), &sm.q_full[x]);
                 }
                 __syncwarp();
             }
@@ -592,7 +605,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                         m_used = mt;
                         l *= alpha;
                     }
-                    const float ref = m_used == kNegInf ? 0.f : m_used;
+                    const float ref = !live ? -kNegInf : m_used == kNegInf ? 0.f : m_used;   // other rows: weights of 0
                     const uint64_t sl2x2 = pack_f32x2(sl2, sl2), negm2 = pack_f32x2(-ref, -ref);
                     uint64_t acc[2] = {0, 0};
 #pragma unroll
@@ -895,7 +908,7 @@ cudaError_t launch_tc(const AttnArgs &a, int num_sms, cudaStream_t st) {
     const uint32_t box = (uint32_t)(a.S < kUnitKeys ? a.S : kUnitKeys);
     if (!make_map_3d(&maps.k, a.k_pages, D, a.S, heads, box) || !make_map_3d(&maps.v, a.v_pages, D, a.S, heads, box) ||
         !make_map_qrows(&maps.q, a.q, a.T, a.Hkv, a.G, D, kTileRows) ||
-        !make_map_qrows(&maps.q_small, a.q, a.T, a.Hkv, a.G, D, tc::kSmallRows))
+        !make_map_qrows(&maps.q_small, a.q, a.T, a.Hkv, a.G, D, tc::kBoxRows))
         return cudaErrorInvalidValue;
     auto kern = tc::shared_attn_tc_kernel<D>;
     const size_t smem = sizeof(tc::Smem<D>) + 1024;
