@@ -30,10 +30,11 @@ namespace shared {
 // 16 threads of a row find its weights, and each half-warp adds 4 keys to a
 // whole 16 x D output, summed over the half-warps at the end; so K and V leave
 // shared memory once per half (64 rows of 2048 local keys: 139 us, a row-wise
-// split that waits for its loads 190).  Longer tiles take 64 rows at a time
-// with 4 x 4 scores a thread, which is bound by the FMA pipe; 17 to 64 rows
-// through the short path in turns of 16 measured slower (44 rows: 64 us
-// against 49).
+// split that waits for its loads 190).  Longer tiles take 32, 48 or 64 rows at a
+// time, 2, 3 or 4 rows x 4 keys of scores a thread, which is bound by the FMA
+// pipe (always 64: 279 us against 251 for 20 rows of a group behind 20000 keys,
+// 49 against 43 for 44 query rows behind 4000); 17 to 64 rows through the short
+// path in turns of 16 measured slower (44 rows: 64 us).
 
 __device__ __forceinline__ float dot4(const float4 &x, const float4 &y, float t) {
     t = fmaf(x.x, y.x, t);
@@ -281,116 +282,125 @@ __device__ void run_few(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
     }
 }
 
-template <int D>
-__device__ void run_many(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
-    constexpr int LD = Smem<D>::LD, LQ = Smem<D>::LQ, LP = Smem<D>::LP, MR = 4, BR = 16 * MR, NC = D / 64;
+// Rows rb .. rb + 16 MR of a tile: a thread has rows rb + ty + 16 i.
+template <int D, int MR>
+__device__ void run_rows(const AttnArgs &a, const Seg &s, Smem<D> &sm, int rb) {
+    constexpr int LD = Smem<D>::LD, LQ = Smem<D>::LQ, LP = Smem<D>::LP, BR = 16 * MR, NC = D / 64;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int rows = s.t.ntok * a.G;
-    for (int rb = 0; rb < rows; rb += BR) {
-        __syncthreads();  // the previous rows are done with the buffers
-        start_keys<D>(a, s.g, half_of(a, s, 2 * s.k), sm.k[0], sm.v[0]);
-        load_queries<D>(a, s, rb, BR, rows, sm.q);
-        float m[MR], l[MR];
-        float4 o[MR][NC];
-        int own[MR];  // local keys the row sees
+    __syncthreads();  // the previous rows are done with the buffers
+    start_keys<D>(a, s.g, half_of(a, s, 2 * s.k), sm.k[0], sm.v[0]);
+    load_queries<D>(a, s, rb, BR, rows, sm.q);
+    float m[MR], l[MR];
+    float4 o[MR][NC];
+    int own[MR];  // local keys the row sees
 #pragma unroll
-        for (int i = 0; i < MR; ++i) {
-            m[i] = kNegInf;
-            l[i] = 0.f;
-            const int rr = rb + ty * MR + i;
-            own[i] = min(s.t.keys, s.t.base + rr / a.G + 1);
+    for (int i = 0; i < MR; ++i) {
+        m[i] = kNegInf;
+        l[i] = 0.f;
+        const int rr = rb + ty + 16 * i;
+        own[i] = min(s.t.keys, s.t.base + rr / a.G + 1);
 #pragma unroll
-            for (int c = 0; c < NC; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        int buf = 1;
-        for (int hu = 2 * s.k; hu < 2 * (s.k + s.n); ++hu) {   // halves of units
-            buf ^= 1;
-            const Half f = half_of(a, s, hu);
-            const bool pre = f.pre;
-            const int kb = f.kb, k1 = f.k1;
-            wait_keys();
-            __syncthreads();  // this half is here, the other buffer free
-            if (hu + 1 < 2 * (s.k + s.n)) start_keys<D>(a, s.g, half_of(a, s, hu + 1), sm.k[buf ^ 1], sm.v[buf ^ 1]);
-            if (kb >= k1) continue;
-            const float *kt = sm.k[buf], *vt = sm.v[buf];
-            float sc[MR][4];
+        for (int c = 0; c < NC; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    int buf = 1;
+    for (int hu = 2 * s.k; hu < 2 * (s.k + s.n); ++hu) {   // halves of units
+        buf ^= 1;
+        const Half f = half_of(a, s, hu);
+        const bool pre = f.pre;
+        const int kb = f.kb, k1 = f.k1;
+        wait_keys();
+        __syncthreads();  // this half is here, the other buffer free
+        if (hu + 1 < 2 * (s.k + s.n)) start_keys<D>(a, s.g, half_of(a, s, hu + 1), sm.k[buf ^ 1], sm.v[buf ^ 1]);
+        if (kb >= k1) continue;
+        const float *kt = sm.k[buf], *vt = sm.v[buf];
+        float sc[MR][4];
 #pragma unroll
-            for (int i = 0; i < MR; ++i)
+        for (int i = 0; i < MR; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) sc[i][j] = 0.f;
+            for (int j = 0; j < 4; ++j) sc[i][j] = 0.f;
 #pragma unroll 4
-            for (int d = 0; d < D; d += 4) {
-                float4 kx[4];
+        for (int d = 0; d < D; d += 4) {
+            float4 kx[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) kx[j] = *reinterpret_cast<const float4 *>(kt + (tx + 16 * j) * LD + d);
-#pragma unroll
-                for (int i = 0; i < MR; ++i) {
-                    const float4 qx = *reinterpret_cast<const float4 *>(sm.q + (ty * MR + i) * LQ + d);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) sc[i][j] = dot4(qx, kx[j], sc[i][j]);
-                }
-            }
-            bool masked = false;
+            for (int j = 0; j < 4; ++j) kx[j] = *reinterpret_cast<const float4 *>(kt + (tx + 16 * j) * LD + d);
 #pragma unroll
             for (int i = 0; i < MR; ++i) {
-                float mx = kNegInf;
-                const int lim = pre ? k1 : own[i];
+                const float4 qx = *reinterpret_cast<const float4 *>(sm.q + (ty + 16 * i) * LQ + d);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (kb + tx + 16 * j >= lim) sc[i][j] = kNegInf;
-                    mx = fmaxf(mx, sc[i][j]);
-                }
-                masked |= kb + kKB > lim;
-#pragma unroll
-                for (int x = 8; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-                const float mn = fmaxf(m[i], mx);
-                const float ref = mn == kNegInf ? 0.f : mn;  // nothing seen yet: every weight is 0
-                const float al = exp2f(m[i] - ref);
-                m[i] = mn;
-                float ps = 0.f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float p = exp2f(sc[i][j] - ref);
-                    ps += p;
-                    sm.p[(ty * MR + i) * LP + tx + 16 * j] = p;
-                }
-#pragma unroll
-                for (int x = 8; x >= 1; x >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, x);
-                l[i] = l[i] * al + ps;
-#pragma unroll
-                for (int c = 0; c < NC; ++c) scale4(al, o[i][c]);
+                for (int j = 0; j < 4; ++j) sc[i][j] = dot4(qx, kx[j], sc[i][j]);
             }
-            __syncwarp();
-            const int kn = min(kKB, k1 - kb);
-            for (int k = 0; k < kn; k += 4) {
-                float4 px[MR];
+        }
+        bool masked = false;
 #pragma unroll
-                for (int i = 0; i < MR; ++i) px[i] = *reinterpret_cast<const float4 *>(sm.p + (ty * MR + i) * LP + k);
+        for (int i = 0; i < MR; ++i) {
+            float mx = kNegInf;
+            const int lim = pre ? k1 : own[i];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+            for (int j = 0; j < 4; ++j) {
+                if (kb + tx + 16 * j >= lim) sc[i][j] = kNegInf;
+                mx = fmaxf(mx, sc[i][j]);
+            }
+            masked |= kb + kKB > lim;
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        const float4 vx = *reinterpret_cast<const float4 *>(vt + (k + e) * LD + 64 * c + 4 * tx);
+            for (int x = 8; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+            const float mn = fmaxf(m[i], mx);
+            const float ref = mn == kNegInf ? 0.f : mn;  // nothing seen yet: every weight is 0
+            const float al = exp2f(m[i] - ref);
+            m[i] = mn;
+            float ps = 0.f;
 #pragma unroll
-                        for (int i = 0; i < MR; ++i) {
-                            const float p = e == 0 ? px[i].x : e == 1 ? px[i].y : e == 2 ? px[i].z : px[i].w;
-                            // a weight of 0 at a key the row does not see must not meet its value
-                            if (masked && p == 0.f) continue;
-                            axpy4(p, vx, o[i][c]);
-                        }
+            for (int j = 0; j < 4; ++j) {
+                const float p = exp2f(sc[i][j] - ref);
+                ps += p;
+                sm.p[(ty + 16 * i) * LP + tx + 16 * j] = p;
+            }
+#pragma unroll
+            for (int x = 8; x >= 1; x >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, x);
+            l[i] = l[i] * al + ps;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) scale4(al, o[i][c]);
+        }
+        __syncwarp();
+        const int kn = min(kKB, k1 - kb);
+        for (int k = 0; k < kn; k += 4) {
+            float4 px[MR];
+#pragma unroll
+            for (int i = 0; i < MR; ++i) px[i] = *reinterpret_cast<const float4 *>(sm.p + (ty + 16 * i) * LP + k);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const float4 vx = *reinterpret_cast<const float4 *>(vt + (k + e) * LD + 64 * c + 4 * tx);
+#pragma unroll
+                    for (int i = 0; i < MR; ++i) {
+                        const float p = e == 0 ? px[i].x : e == 1 ? px[i].y : e == 2 ? px[i].z : px[i].w;
+                        // a weight of 0 at a key the row does not see must not meet its value
+                        if (masked && p == 0.f) continue;
+                        axpy4(p, vx, o[i][c]);
                     }
                 }
             }
-            __syncwarp();
         }
+        __syncwarp();
+    }
 #pragma unroll
-        for (int i = 0; i < MR; ++i) {
-            const int rr = rb + ty * MR + i;
-            if (rr >= rows) continue;
+    for (int i = 0; i < MR; ++i) {
+        const int rr = rb + ty + 16 * i;
+        if (rr >= rows) continue;
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-                store_row<D>(a, s, rows, rr, 64 * c + 4 * tx, o[i][c], m[i], l[i], c == 0 && tx == 0);
-        }
+        for (int c = 0; c < NC; ++c)
+            store_row<D>(a, s, rows, rr, 64 * c + 4 * tx, o[i][c], m[i], l[i], c == 0 && tx == 0);
+    }
+}
+
+template <int D>
+__device__ void run_many(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
+    const int rows = s.t.ntok * a.G;
+    for (int rb = 0; rb < rows; rb += 64) {
+        if (rows - rb <= 32) run_rows<D, 2>(a, s, sm, rb);
+        else if (rows - rb <= 48) run_rows<D, 3>(a, s, sm, rb);
+        else run_rows<D, 4>(a, s, sm, rb);
     }
 }
 
