@@ -614,8 +614,11 @@ asm_status asm_rope_append(const void *q, int64_t q_st, int64_t q_sh,
  * Offsets that fall are raised to the largest before them, offsets and
  * lengths beyond T, R, the tables' pages are clamped.
  *   plan       asm_shared_plan_size(R, NG, T, Hq, Hkv) bytes (any content)
- * NG <= 4096, T <= 2^24.  The plan belongs to these sizes and to the device it
- * was made on; any number of calls may read it.  One launch.
+ * NG <= 4096, T <= 2^24; page_size x max_pages and page_size x
+ * max_prefix_pages at most 2^30 (ASM_ERR_INVALID_ARG).  The plan belongs to these
+ * sizes and to the device it was made on; any number of calls may read it.  Work
+ * of more than about 2^29 units (128 keys of a tile and KV head) per SM gives a
+ * plan that asm_shared_attention refuses.  One launch.
  */
 size_t asm_shared_plan_size(int R, int NG, int T, int Hq, int Hkv);
 asm_status asm_shared_plan(const int32_t *q_off, const int32_t *seq_len,
@@ -643,7 +646,8 @@ asm_status asm_shared_plan(const int32_t *q_off, const int32_t *seq_len,
  * A token without any key gets (0, -inf).  Tokens outside every row are left
  * as they were.  Keys that a token does not see (later tokens, places behind a
  * row's length) never reach its result, whatever their pages hold, infinities
- * and NaN among it.  A page id outside [0, n_pages) reads as zeros and sets the
+ * and NaN among it; non-finite values that it does see are summed apart, which
+ * is slow.  A page id outside [0, n_pages) reads as zeros and sets the
  * error word to ASM_ERR_INVALID_ARG, and so does a plan of other sizes, with
  * which the call writes nothing; a device-side wait that gives up sets
  * ASM_ERR_TIMEOUT (outputs not valid).  (out, lse_out) is an attention state:

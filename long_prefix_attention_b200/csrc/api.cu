@@ -464,6 +464,9 @@ asm_status asm_rope_append(const void *q, int64_t q_st, int64_t q_sh, const void
                                               v_pages, n_pages, page_size, num_sms(), stream));
 }
 
+// n pages of one key list: a unit's end, and the cost of a list, stay within int32
+static bool list_fits(int n, int S) { return n >= 1 && (int64_t)n * S <= (1 << 30); }
+
 // sizes of a shared-attention plan
 static asm_status shared_sizes(int R, int NG, int T, int Hq, int Hkv) {
     if (R < 1 || NG < 0 || T < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return ASM_ERR_INVALID_ARG;
@@ -482,7 +485,7 @@ asm_status asm_shared_plan(const int32_t *q_off, const int32_t *seq_len, const i
     const asm_status v = shared_sizes(R, NG, T, Hq, Hkv);
     if (v != ASM_OK) return v;
     if (!page_ok(page_size)) return ASM_ERR_UNSUPPORTED;
-    if (!pages_fit(max_pages, page_size) || (NG > 0 && !pages_fit(max_prefix_pages, page_size)))
+    if (!list_fits(max_pages, page_size) || (NG > 0 && !list_fits(max_prefix_pages, page_size)))
         return ASM_ERR_INVALID_ARG;
     if (!aligned(q_off, 4) || !aligned(seq_len, 4)) return ASM_ERR_INVALID_ARG;
     if (NG > 0 && (!aligned(group_off, 4) || !aligned(prefix_len, 4))) return ASM_ERR_INVALID_ARG;
@@ -505,8 +508,8 @@ asm_status asm_shared_attention(const void *q, const void *k_pages, const void *
     if (v != ASM_OK) return v;
     if (!dt_ok(dt) || !(scale > 0.f) || !(scale < 1e30f)) return ASM_ERR_INVALID_ARG;
     if (!d_ok(d) || !page_ok(page_size)) return ASM_ERR_UNSUPPORTED;
-    if (!pages_fit(n_pages, page_size) || !pages_fit(max_pages, page_size) ||
-        (NG > 0 && !pages_fit(max_prefix_pages, page_size)) || (int64_t)n_pages * Hkv > INT32_MAX)
+    if (!pages_fit(n_pages, page_size) || !list_fits(max_pages, page_size) ||
+        (NG > 0 && !list_fits(max_prefix_pages, page_size)) || (int64_t)n_pages * Hkv > INT32_MAX)
         return ASM_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(table, 4) || !aligned(out, 16))
         return ASM_ERR_INVALID_ARG;

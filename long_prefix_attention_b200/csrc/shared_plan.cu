@@ -192,7 +192,7 @@ shared_plan_kernel(const PlanArgs a) {
     long long range = (W + a.workers - 1) / a.workers;
     const int dearest = cost_unit(__syncthreads_or(tall) ? kDualRows : kTileRows);
     range = range < dearest ? dearest : range;
-    if (range > INT32_MAX) range = INT32_MAX;     // a table cannot be that long
+    const bool too_long = range > INT32_MAX;      // hours of work: no plan (the attention refuses a header without its magic)
     // ---- partial rows before each tile
     before = 0;
     for (int c = 0; c < ntiles; c += kPlanThreads) {
@@ -209,7 +209,7 @@ shared_plan_kernel(const PlanArgs a) {
             tiles[i].row0 = before + inc - rows;
             // the workers whose ranges begin in this tile
             const long long c0 = tiles[i].cost0 * a.Hkv, c1 = c0 + cost_of(tiles[i].ntok * G, tiles[i].units) * a.Hkv;
-            for (long long w = (c0 + range - 1) / range; w * range < c1; ++w) first[w] = i;
+            for (long long w = (c0 + range - 1) / range; !too_long && w * range < c1; ++w) first[w] = i;
         }
         before += tot;
     }
@@ -230,7 +230,7 @@ shared_plan_kernel(const PlanArgs a) {
     }
     if (tid == 0) {
         Header h{};
-        h.magic = kMagic;
+        h.magic = too_long ? 0 : kMagic;
         h.R = R; h.NG = NG; h.T = a.T; h.Hq = a.Hq; h.Hkv = a.Hkv;
         h.page_size = a.S; h.max_pages = a.max_pages; h.max_prefix_pages = a.max_prefix_pages;
         h.workers = a.workers; h.ntiles = ntiles; h.range = (int)range; h.W = W; h.inv_range = 1.0 / (double)range;

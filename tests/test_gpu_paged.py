@@ -496,6 +496,23 @@ def test_plan_survives_falling_offsets():
         ops.asm_workspace_error(ws)
 
 
+@pytest.mark.parametrize("tokens", [2**30, 2**27])
+def test_a_plan_of_too_much_work_is_marked(tokens):
+    """131072 new tokens of one row, 32 KV heads, behind 2^30 keys: 512 tiles x 32 x
+    2^23 units of cost 4 are 3.7e9 per worker, above 2^31: the plan's first word, which
+    the attention checks, is 0, and nothing is written behind the plan.  2^27 keys are
+    an eighth of it, and planned."""
+    T, H, S = 131072, 32, 128
+    n = ops.asm_shared_plan_size(1, 1, T, H, H)
+    plan = torch.full((n + 65536,), 0x5a, dtype=torch.uint8, device="cuda")
+    table = torch.zeros(1, T // S, dtype=torch.int32, device="cuda")
+    ptable = torch.zeros(1, tokens // S, dtype=torch.int32, device="cuda")
+    ops.asm_shared_plan(i32([0, T]), i32([T]), table, T, H, H, S, plan[:n], group_off=i32([0, 1]),
+                        prefix_len=i32([tokens]), prefix_table=ptable)
+    assert (int(plan[:4].cpu().numpy().view(np.int32)[0]) == 0) == (tokens == 2**30)
+    assert (plan[n:] == 0x5a).all()
+
+
 @pytest.mark.parametrize("tok", [8, 9, 12, 16, 17])
 def test_a_later_token_never_reaches_an_earlier_draft(tok):
     """As above, for tiles of 32 to 68 query rows, the bad key in either half of a unit."""

@@ -146,6 +146,15 @@ def test_binding_refuses_host_tensors_and_other_types():
         ops._i32("f", i.long())
 
 
+def test_key_lists_are_at_most_2_to_30(lib):
+    """A unit's last key plus one unit stays within int32."""
+    assert plan(lib, MP=(1 << 26) + 1) == INVALID and plan(lib, MPP=(1 << 26) + 1) == INVALID
+    assert attn(lib, MP=(1 << 26) + 1) == INVALID and attn(lib, MPP=(1 << 26) + 1) == INVALID
+    # the limit itself passes on to the next check
+    assert plan(lib, MP=1 << 26, MPP=1 << 26, nb=16) == WORKSPACE
+    assert attn(lib, MP=1 << 26, MPP=1 << 26, pb=16) == WORKSPACE
+
+
 def plan_tiles(new, old, pre, cuts, G):
     """The tiles of a plan, (query rows per KV head, units) each, as the plan
     kernel lays them out: prefix tiles over the runs of rows of up to 128 query
