@@ -384,13 +384,17 @@ asm_status asm_page_step(const int32_t *kv_len, const int32_t *new_len, const in
     if (pos_base && !aligned(pos_base, 4)) return ASM_ERR_INVALID_ARG;
     if (T > 0 && (!aligned(row, 4) || !aligned(pos, 4) || !aligned(slot, 4))) return ASM_ERR_INVALID_ARG;
     // every block reads the inputs: none of them may be an output
-    const void *in[4] = {kv_len, new_len, pos_base, pool_state};
-    const size_t in_n[4] = {(size_t)R, (size_t)R, pos_base ? (size_t)R : 0, 3};
+    const void *in[6] = {kv_len, new_len, pos_base, pool_state, table, pool};
+    const size_t in_n[6] = {(size_t)R, (size_t)R, pos_base ? (size_t)R : 0, 3, (size_t)R * max_pages, (size_t)F};
     const void *out[6] = {seq_len, q_off, row, pos, slot, pool_out};
     const size_t out_n[6] = {(size_t)R, (size_t)R + 1, (size_t)T, (size_t)T, (size_t)T, 3};
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 6; ++i)
         for (int o = 0; o < 6; ++o)
             if (overlap(in[i], 4 * in_n[i], out[o], 4 * out_n[o])) return ASM_ERR_INVALID_ARG;
+    // the table and the ring change in the call as well
+    for (int i = 0; i < 5; ++i)
+        for (int o = 4; o < 6; ++o)
+            if (i < o && overlap(in[i], 4 * in_n[i], in[o], 4 * in_n[o])) return ASM_ERR_INVALID_ARG;
     return cuda_status(asm_page_step_launch(kv_len, new_len, pos_base, R, page_size, max_pages, table, pool,
                                             pool_state, F, T, seq_len, q_off, row, pos, slot, pool_out, num_sms(),
                                             stream));

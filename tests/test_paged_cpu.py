@@ -45,6 +45,12 @@ def test_page_step_refusals(lib):
     assert page_step(lib, R=4097) == UNSUPPORTED
 
 
+def test_page_step_refuses_a_table_or_ring_within_other_arrays(lib):
+    for kw in (dict(seq=at(3, 4)), dict(pout=at(4, 8)), dict(slot=at(3, 124)), dict(kv=at(3)), dict(new=at(4)),
+               dict(base=at(3, 16)), dict(state=at(4, 252)), dict(table=at(4, 128)), dict(pool=at(3, 64))):
+        assert page_step(lib, **kw) == INVALID, kw
+
+
 def rope(lib, **kw):
     a = dict(x=at(0), xt=512, xh=128, T=5, H=4, d=128, dt=1, pos=at(1), f=at(2), rot=128, lay=0, ms=1.0, inv=0, y=at(3),
              yt=512, yh=128)
