@@ -13,7 +13,8 @@
 // which finds its row by bisection.  Nothing read is written in the same
 // call (the ring's taken and returned places are disjoint), so a call can be
 // repeated on the same inputs.  Bound by latency: two dependent trips to
-// memory, the lengths and a token's page.
+// memory, the lengths and a token's page (16 rows 5.0 us in a captured graph,
+// 1500 rows 9.4).
 #include <cuda_runtime.h>
 #include <stdint.h>
 

