@@ -4,8 +4,10 @@
 // One block: running maxima make the offsets monotone whatever they hold,
 // then sums over the rows, the runs of rows that share prefix tiles and the
 // tiles give the tile list, the cost and the partial rows before each tile.  Bound by
-// latency: some ten sums over the block, one after the other (12 us for 16 to 64
-// rows, 14 for 600, 56 for 4096); a step's layers share one plan.
+// latency: some ten sums over the block, one after the other (10 us for 16 to 64
+// rows, 14 for 600, 56 for 4096); a step's layers share one plan.  A step of few
+// rows and tokens takes 128 threads, whose sums are shorter (16 rows: 10.1 us, with
+// 1024 threads 12.2), longer ones 1024.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -16,7 +18,8 @@
 namespace asmk {
 namespace shared {
 
-constexpr int kPlanThreads = 1024;
+
+constexpr int kSmallPlan = 128;   // threads of a small step's plan
 
 struct PlanArgs {
     const int *q_off, *seq_len, *group_off, *prefix_len;
@@ -24,7 +27,8 @@ struct PlanArgs {
     char *plan;
 };
 
-template <typename Op>
+// N threads.
+template <int N, typename Op>
 __device__ __forceinline__ long long plan_scan(long long v, long long *warp_v, long long zero, long long &tot, Op op) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -36,16 +40,16 @@ __device__ __forceinline__ long long plan_scan(long long v, long long *warp_v, l
     if (lane == 31) warp_v[warp] = v;
     __syncthreads();
     if (warp == 0) {
-        long long w = warp_v[lane];
+        long long w = lane < N / 32 ? warp_v[lane] : zero;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
             const long long o = __shfl_up_sync(0xffffffffu, w, m);
             if (lane >= m) w = op(o, w);
         }
-        warp_v[lane] = w;
+        if (lane < N / 32) warp_v[lane] = w;
     }
     __syncthreads();
-    tot = warp_v[31];
+    tot = warp_v[N / 32 - 1];
     return warp > 0 ? op(warp_v[warp - 1], v) : op(zero, v);
 }
 
@@ -61,13 +65,14 @@ __device__ __forceinline__ int first_above(const int *ends, int n, int x) {
 }
 
 // off[0..n] = running maxima of src, kept within [0, hi].
+template <int N>
 __device__ void monotone(const int *src, int *off, int n, int hi, long long *warp_v) {
-    const int per = (n + 1 + kPlanThreads - 1) / kPlanThreads, i0 = threadIdx.x * per;
+    const int per = (n + 1 + N - 1) / N, i0 = threadIdx.x * per;
     long long m = 0, tot;
     for (int i = i0; i < i0 + per && i <= n; ++i) m = max(m, (long long)min(max(src[i], 0), hi));
-    const long long inc = plan_scan(m, warp_v, 0, tot, [](long long a, long long b) { return max(a, b); });
+    const long long inc = plan_scan<N>(m, warp_v, 0, tot, [](long long a, long long b) { return max(a, b); });
     // the maximum before this thread's entries: the inclusive one of its left neighbour
-    __shared__ int left[kPlanThreads];
+    __shared__ int left[N];
     left[threadIdx.x] = (int)inc;
     __syncthreads();
     int run = threadIdx.x > 0 ? left[threadIdx.x - 1] : 0;
@@ -78,7 +83,8 @@ __device__ void monotone(const int *src, int *off, int n, int hi, long long *war
     __syncthreads();
 }
 
-__global__ void __launch_bounds__(kPlanThreads)
+template <int N>
+__global__ void __launch_bounds__(N)
 shared_plan_kernel(const PlanArgs a) {
     extern __shared__ int sm[];
     __shared__ long long warp_v[32];
@@ -95,8 +101,8 @@ shared_plan_kernel(const PlanArgs a) {
     const int dual = kDualRows / G;  // tokens of a 256-row tile
     const int single = kTileRows / G;
 
-    monotone(a.q_off, qo, R, a.T, warp_v);
-    if (NG > 0) monotone(a.group_off, go, NG, R, warp_v);
+    monotone<N>(a.q_off, qo, R, a.T, warp_v);
+    if (NG > 0) monotone<N>(a.group_off, go, NG, R, warp_v);
     // tiles of n tokens: one of up to 128 query rows, else 256-row ones
     auto n_tiles = [&](int n) { return n <= 0 ? 0 : n <= single ? 1 : (n + dual - 1) / dual; };
     // group of a row, -1 for none
@@ -112,12 +118,12 @@ shared_plan_kernel(const PlanArgs a) {
     auto starts_run = [&](int r, int g) {
         return g >= 0 && !tall_row(r) && (r == go[g] || tall_row(r - 1));
     };
-    const int per = (R + kPlanThreads - 1) / kPlanThreads, r0 = tid * per, r1 = min(r0 + per, R);
+    const int per = (R + N - 1) / N, r0 = tid * per, r1 = min(r0 + per, R);
     long long tot, n_runs, n_prefix;
     {
         long long s = 0;
         for (int r = r0; r < r1; ++r) s += starts_run(r, group_of(r));
-        long long e = plan_scan(s, warp_v, 0, n_runs, add) - s;
+        long long e = plan_scan<N>(s, warp_v, 0, n_runs, add) - s;
         for (int r = r0; r < r1; ++r) {
             const int g = group_of(r);
             if (starts_run(r, g)) run_lo[e++] = r;
@@ -131,7 +137,7 @@ shared_plan_kernel(const PlanArgs a) {
     {
         long long s = 0;
         for (int i = r0; i < min(r0 + per, (int)n_runs); ++i) s += n_tiles(qo[run_hi[i]] - qo[run_lo[i]]);
-        long long e = plan_scan(s, warp_v, 0, n_prefix, add) - s;
+        long long e = plan_scan<N>(s, warp_v, 0, n_prefix, add) - s;
         for (int i = r0; i < min(r0 + per, (int)n_runs); ++i) {
             e += n_tiles(qo[run_hi[i]] - qo[run_lo[i]]);
             run_end[i] = (int)e;
@@ -140,7 +146,7 @@ shared_plan_kernel(const PlanArgs a) {
     {
         long long s = 0;
         for (int r = r0; r < r1; ++r) s += n_tiles(qo[r + 1] - qo[r]);
-        long long e = n_prefix + plan_scan(s, warp_v, 0, tot, add) - s;
+        long long e = n_prefix + plan_scan<N>(s, warp_v, 0, tot, add) - s;
         for (int r = r0; r < r1; ++r) {
             e += n_tiles(qo[r + 1] - qo[r]);
             row_end[r] = (int)e;
@@ -151,7 +157,7 @@ shared_plan_kernel(const PlanArgs a) {
     // ---- the tiles, and the cost before each (chunks of one tile a thread)
     long long before = 0;
     int tall = 0;
-    for (int c = 0; c < ntiles; c += kPlanThreads) {
+    for (int c = 0; c < ntiles; c += N) {
         const int i = c + tid;
         Tile t{};
         if (i < ntiles) {
@@ -183,7 +189,7 @@ shared_plan_kernel(const PlanArgs a) {
             t.units = (t.pre_keys + kUnitKeys - 1) / kUnitKeys + (t.keys + kUnitKeys - 1) / kUnitKeys;
         }
         const long long cost = cost_of(t.ntok * G, t.units);
-        const long long inc = plan_scan(cost, warp_v, 0, tot, add);
+        const long long inc = plan_scan<N>(cost, warp_v, 0, tot, add);
         t.cost0 = before + inc - cost;
         before += tot;
         tall |= t.ntok * G > kTileRows;
@@ -196,7 +202,7 @@ shared_plan_kernel(const PlanArgs a) {
     const bool too_long = range > INT32_MAX;      // hours of work: no plan (the attention refuses a header without its magic)
     // ---- partial rows before each tile
     before = 0;
-    for (int c = 0; c < ntiles; c += kPlanThreads) {
+    for (int c = 0; c < ntiles; c += N) {
         const int i = c + tid;
         long long rows = 0;
         int cap = 0;
@@ -204,7 +210,7 @@ shared_plan_kernel(const PlanArgs a) {
             cap = (int)(cost_of(tiles[i].ntok * G, tiles[i].units) / range) + 2;
             rows = (long long)cap * a.Hkv * tiles[i].ntok * G;
         }
-        const long long inc = plan_scan(rows, warp_v, 0, tot, add);
+        const long long inc = plan_scan<N>(rows, warp_v, 0, tot, add);
         if (i < ntiles) {
             tiles[i].cap = cap;
             tiles[i].row0 = before + inc - rows;
@@ -215,7 +221,7 @@ shared_plan_kernel(const PlanArgs a) {
         before += tot;
     }
     // ---- the tiles of every token
-    for (int t = tid; t < a.T; t += kPlanThreads) {
+    for (int t = tid; t < a.T; t += N) {
         int2 v = make_int2(-1, -1);
         if (t >= qo[0] && t < qo[R]) {
             const int r = first_above(qo + 1, R, t);
@@ -239,6 +245,18 @@ shared_plan_kernel(const PlanArgs a) {
     }
 }
 
+template <int N>
+cudaError_t launch_plan(const PlanArgs &a, cudaStream_t st) {
+    const size_t smem = sizeof(int) * (6 * (size_t)a.R + (size_t)a.NG + 2);
+    if (smem > 40 * 1024) {  // beside the static arrays
+        cudaError_t e = cudaFuncSetAttribute(shared_plan_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (7 * kMaxRows + 2) * (int)sizeof(int));
+        if (e != cudaSuccess) return e;
+    }
+    shared_plan_kernel<N><<<1, N, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
 }  // namespace shared
 }  // namespace asmk
 
@@ -256,12 +274,6 @@ cudaError_t asm_shared_plan_launch(const int32_t *q_off, const int32_t *seq_len,
     a.S = page_size; a.max_pages = max_pages; a.max_prefix_pages = max_prefix_pages;
     a.workers = num_sms < kMaxWorkers ? num_sms : kMaxWorkers;
     a.plan = static_cast<char *>(plan);
-    const size_t smem = sizeof(int) * (6 * (size_t)R + (size_t)NG + 2);
-    if (smem > 40 * 1024) {  // beside the static arrays
-        cudaError_t e = cudaFuncSetAttribute(shared_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (7 * kMaxRows + 2) * (int)sizeof(int));
-        if (e != cudaSuccess) return e;
-    }
-    shared_plan_kernel<<<1, kPlanThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    if (R <= kSmallPlan && T <= 2 * kSmallPlan) return launch_plan<kSmallPlan>(a, st);
+    return launch_plan<1024>(a, st);
 }

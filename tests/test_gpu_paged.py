@@ -535,6 +535,26 @@ def test_shared_attention_repeats_bit_for_bit():
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_two_calls_at_once(dt):
+    """Calls on two streams, with a workspace and a plan each, do not disturb one another."""
+    both = [Batch(dt, 8, 2, 128, 32, new=[1] * 20, seq=[100 + 7 * i for i in range(20)], goff=[0, 20], pre=[1500], seed=21),
+            Batch(dt, 4, 2, 128, 64, new=[150, 1, 5], seq=[400, 700, 60], goff=[0, 3], pre=[260], seed=22)]
+    alone = [b.run() for b in both]
+    ws, q, streams = [b.ws() for b in both], [b.q.cuda() for b in both], [torch.cuda.Stream() for _ in both]
+    plans, outs = [b.plan() for b in both], [[torch.empty_like(x) for _ in range(8)] for x in q]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for j, b in enumerate(both):
+            ops.asm_shared_attention(q[j], b.kd, b.vd, b.dev["table"], plans[j], b.scale, outs[j][i], ws[j],
+                                     prefix_table=b.dev["prefix_table"], stream=streams[j])
+    torch.cuda.synchronize()
+    for j in (0, 1):
+        assert ops.asm_workspace_error(ws[j]) == 0
+        for o in outs[j]:
+            assert torch.equal(o[:both[j].q_off[-1]], alone[j][0][:both[j].q_off[-1]])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_captured_steps_follow_the_lengths(dt):
     """One graph of plan and two layers, replayed with other lengths, and the
     same calls on a second stream at once with their own workspace."""
