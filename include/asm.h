@@ -643,8 +643,9 @@ asm_status asm_shared_plan(const int32_t *q_off, const int32_t *seq_len,
  *   ws           asm_shared_attention_workspace_size(...) bytes, word 0 zeroed
  *                once (asm_workspace_init); asm_workspace_error reads it.  It
  *                grows with T x Hq (partial states of the rows)
- * A token without any key gets (0, -inf).  Tokens outside every row are left
- * as they were.  Keys that a token does not see (later tokens, places behind a
+ * A token without any key, or whose scores are all -inf, gets (0, -inf); a
+ * score of +inf gives NaN, as in the formula.  Tokens outside every row are
+ * left as they were.  Keys that a token does not see (later tokens, places behind a
  * row's length) never reach its result, whatever their pages hold, infinities
  * and NaN among it; non-finite values that it does see are summed apart, which
  * is slow.  A page id outside [0, n_pages) reads as zeros and sets the

@@ -125,7 +125,8 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 
 // 2^t for two arguments on the FMA pipe: t = n + f, f in [-1/2, 1/2], 2^f by a
 // polynomial of degree 5 fitted to it there (relative error 1.6e-7), 2^n
-// added into the exponent.  t is clamped at -125.
+// added into the exponent.  t is clamped at -125, and so are a NaN and -infinity: the
+// caller mends the sums of rows whose maximum is not finite.
 __device__ __forceinline__ uint64_t exp2_poly_x2(uint64_t t2) {
     const uint64_t t = pack_f32x2(fmaxf(lo_f32(t2), -125.f), fmaxf(hi_f32(t2), -125.f));
     const uint64_t y = add_f32x2(t, pack_f32x2(12582912.f, 12582912.f));   // 1.5 * 2^23: n in the low bits
@@ -799,6 +800,11 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 mbar_arrive(&sm.p_full[x]);
             }
             // ------------------------------------------------------ epilogue
+            // The polynomial's clamp has lost the NaN of a score of +inf (inf - inf) and the
+            // zero weights of rows that saw scores of -inf alone.  A vote per unit that keeps
+            // such rows off the polynomial costs tall tiles 2.8%.
+            if (m_used == -kNegInf) l = m_used - m_used;
+            if (m_used == kNegInf) l = 0.f;
             if (joint) {
                 sm.ml[x][row] = make_float2(m_used, l);
                 wait(&sm.o_full[0], on[0] & 1);
