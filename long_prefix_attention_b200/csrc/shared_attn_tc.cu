@@ -42,7 +42,10 @@
 // S_1 / P_1 [384,512).  A stream's products complete in issue order, so S_x(next)
 // (issued after P_x V) overwrites P_x only once it was read, and its completion
 // means that O_x is stable.  Every wait is bounded; after a timeout a warp waits no
-// more, keeps to the barriers it shares with others, and the error word is set.
+// more and arrives at no mbarrier, so that the others run out too, and the error word
+// is set.  The named barriers have no limit, so the softmax warps pass the same ones
+// whatever has timed out: they follow the list of segments to its end, which a producer
+// that gives up publishes as well.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -84,6 +87,10 @@ struct Cfg {
 // it enters a segment only when the ring has taken all of the one before, so
 // at most RING / 2 + 3 segments are in use at a time.
 constexpr int kSegs = 16;
+// Limits a softmax warp waits for the next segment: a producer in trouble takes one
+// to give up and publish the end, and a warp that left before would leave the others at
+// a barrier.
+constexpr int kSegWaits = 64;
 struct __align__(16) SegDesc {
     int tok0, rows, base, keys;      // first token, query rows; as in Tile
     int g, k, n, pre_keys;           // KV head, first unit, units; as in Tile
@@ -377,6 +384,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 }
             }
         }
+        if (some) publish(ns, false);     // given up: the list ends here
         // every copy that was issued has landed before the CTA may end
         for (uint32_t i = n > RING ? n - RING : 0; i < n; ++i)
             if (!mbar_wait(&sm.kv_full[i % RING], (i / RING) & 1)) ok = false;
@@ -495,8 +503,10 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
         uint32_t sn = 0, on[2] = {0, 0};    // scores taken, outputs finished in each stream
         uint32_t step = 0, unit0 = 0;       // steps and units before this segment
         for (uint32_t seg = 0;; ++seg) {
-            // read to its end even after a timeout: the streams meet at barriers
-            const bool got = __all_sync(0xffffffffu, mbar_wait(&sm.seg_full[seg % kSegs], (seg / kSegs) & 1));
+            // read to its end even after a timeout: the warps meet at barriers
+            bool got = false;
+            for (int i = 0; i < kSegWaits && !got; ++i)
+                got = __all_sync(0xffffffffu, mbar_wait(&sm.seg_full[seg % kSegs], (seg / kSegs) & 1));
             const SegDesc &s = sm.seg[seg % kSegs];
             const int n = got ? s.n : 0;
             ok = ok && got;
@@ -630,7 +640,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                     tmem_wait_st();
                     clean(j);
                     tc_fence_before();
-                    mbar_arrive(&sm.p_full[x]);
+                    if (ok) mbar_arrive(&sm.p_full[x]);
                 }
                 // the states of the quarters, of both streams if both have some, become one
                 sm.ml[x][row] = make_float2(m_used, l);
@@ -764,7 +774,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                     uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
-                        if (c == 0 && dual && st == 0 && (x == 0 || j + 1 < n))
+                        if (c == 0 && dual && st == 0 && ok && (x == 0 || j + 1 < n))
                             mbar_arrive(&sm.turn[x ^ 1][(item0 / 2 + (uint32_t)(j + x)) % (RING / 2)]);
                         uint32_t v[32], pk[16];
                         tmem_ld32(t_s + (uint32_t)(32 * c), v);
@@ -797,7 +807,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 }
                 clean(j);
                 tc_fence_before();
-                mbar_arrive(&sm.p_full[x]);
+                if (ok) mbar_arrive(&sm.p_full[x]);
             }
             // ------------------------------------------------------ epilogue
             // The polynomial's clamp has lost the NaN of a score of +inf (inf - inf) and the
