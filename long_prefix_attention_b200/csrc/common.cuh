@@ -15,10 +15,13 @@ constexpr float kNegInf = -__builtin_huge_valf();
 
 // Bounded spins: a wait that has not completed after this many polls gives
 // up and raises ASM_ERR_TIMEOUT in the caller's error word.  A poll of an
-// mbarrier that does not complete suspends the thread for about 4 us on
-// this part (measured by the timeout self-test), so the bound is about one
-// second, thousands of times any wait of a working kernel.
+// mbarrier that does not complete suspends a whole warp for about 4 us on
+// this part (measured by the timeout self-test): a bound of about one second.
+// One lane that polls while the others of its warp are elsewhere is not
+// suspended (74 ns a poll): a bound of 19 ms, thousands of times the waits of
+// a working kernel, or about a second with kLoneSpinLimit.
 constexpr uint32_t kSpinLimit = 1u << 18;
+constexpr uint32_t kLoneSpinLimit = 1u << 24;
 
 // ---------------------------------------------------------------- dtypes --
 
@@ -171,6 +174,13 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
 // Bounded wait on an mbarrier phase; returns false on timeout.
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
     for (uint32_t i = 0; i < kSpinLimit; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return false;
+}
+
+// The same for one lane that waits while others may work for long.
+__device__ __forceinline__ bool mbar_wait_lone(uint64_t *bar, uint32_t parity) {
+    for (uint32_t i = 0; i < kLoneSpinLimit; ++i)
         if (mbar_try_wait(bar, parity)) return true;
     return false;
 }

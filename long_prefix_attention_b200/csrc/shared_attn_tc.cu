@@ -49,6 +49,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -106,12 +107,16 @@ struct Smem {
     SegDesc seg[kSegs];
     float2 ml[2][128];                 // a row's (max, sum) in each stream
     float4 wl[8][kSmallRows];          // short tiles: a warp's (factor, share of the sum, maximum) of a row
-    float ex[8][512];                  // short tiles: the warps' outputs on their way to one sum
-    uint32_t fix[kFix][kFixUnits][4];  // per segment (modulo kFix): keys whose V was cleared, from the first masked unit on
+    alignas(16) float ex[8][512];      // short tiles: the warps' outputs on their way to one sum
+    uint32_t kinds[2][D / 8];          // short tiles: non-finite values among 8 columns: +inf, -inf << 8, NaN << 16
+    alignas(16) uint32_t fix[kFix][kFixUnits][4];  // per segment (modulo kFix): keys whose V was cleared, from the first masked unit on
     uint64_t kv_full[Cfg<D>::RING], kv_empty[Cfg<D>::RING];
     uint64_t seg_full[kSegs], turn[2][Cfg<D>::RING / 2], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
     uint32_t tmem_base;
 };
+// read and written 16 bytes at a time
+static_assert(offsetof(Smem<64>, ex) % 16 == 0 && offsetof(Smem<64>, fix) % 16 == 0, "alignment");
+static_assert(offsetof(Smem<128>, ex) % 16 == 0 && offsetof(Smem<128>, fix) % 16 == 0, "alignment");
 
 struct Maps {
     CUtensorMap k, v, q, q_small;
@@ -152,6 +157,36 @@ __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, %0;" 
 __device__ __forceinline__ void stream_sync(int x) {
     if (x == 0) asm volatile("bar.sync 2, 128;" ::: "memory");
     else asm volatile("bar.sync 3, 128;" ::: "memory");
+}
+
+// The same, with the or of a condition of all threads.
+__device__ __forceinline__ bool softmax_any(bool c) {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+                 : "=r"(r) : "r"((uint32_t)c), "n"(kSoftmax) : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ bool stream_any(int x, bool c) {
+    uint32_t r;
+    if (x == 0)
+        asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.or.pred q, 2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+                     : "=r"(r) : "r"((uint32_t)c) : "memory");
+    else
+        asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.or.pred q, 3, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+                     : "=r"(r) : "r"((uint32_t)c) : "memory");
+    return r != 0;
+}
+
+// Which of 8 bf16 values are +inf, -inf (<< 8) and NaN (<< 16).
+__device__ __forceinline__ uint32_t non_finite(const uint4 &x) {
+    const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t h = (i & 1) ? y[i >> 1] >> 16 : y[i >> 1] & 0xffffu;
+        if ((h & 0x7f80u) == 0x7f80u) r |= 1u << (i + ((h & 0x7fu) ? 16 : (h & 0x8000u) ? 8 : 0));
+    }
+    return r;
 }
 
 __device__ __forceinline__ int units_of(int keys) { return (keys + kUnitKeys - 1) / kUnitKeys; }
@@ -402,7 +437,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
             const uint64_t q_desc = desc_k_sw128(smem_addr(sm.q[0])), k_desc = desc_k_sw128(smem_addr(sm.kv[0])),
                            v_desc = desc_mn_sw128(smem_addr(sm.kv[0]), kBox);
             const uint32_t t_o = tmem + (uint32_t)(x * 128), t_s = t_o + 256;
-            auto wait1 = [&](uint64_t *bar, uint32_t parity) { ok = ok && mbar_wait(bar, parity); };
+            auto wait1 = [&](uint64_t *bar, uint32_t parity) { ok = ok && mbar_wait_lone(bar, parity); };
             // this stream's steps: unit j of a segment of n, every dj-th
             int n = 0, j = 0, dj = 1, qb = 0, next_qb = 0;
             uint32_t segs = 0, step = 0, unit0 = 0;     // before the segment
@@ -567,32 +602,6 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 }
             };
 
-            // o[i]: the sum of the non-finite values, if there are any, of column c + i over
-            // the segment's prefix keys and its local keys before `own`
-            auto sum_non_finite = [&](int own, int c, float (&o)[4]) {
-                const int *pre_list = a.prefix_table + (size_t)s.group * a.max_prefix_pages;
-                const int *own_list = a.table + (size_t)s.row * a.max_pages;
-                float t[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-                for (int u = k0; u < k0 + n; ++u) {
-                    const int key0 = (u < pu ? u : u - pu) * kUnitKeys, end = min(u < pu ? pre_keys : own, key0 + kUnitKeys);
-#pragma unroll 1
-                    for (int key = key0; key < end; ++key) {
-                        const int id = (u < pu ? pre_list : own_list)[key >> a.shift];
-                        if (id < 0 || id >= a.n_pages) continue;
-                        float y[4];
-                        load_vec<__nv_bfloat16, 4>(static_cast<const __nv_bfloat16 *>(a.v_pages) +
-                            ((((long long)id * a.Hkv + s.g) << a.shift) + (key & (a.S - 1))) * D + c, y);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (!(y[i] - y[i] == 0.f)) t[i] += y[i];
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (t[i] != 0.f) o[i] = t[i];   // a NaN is not 0 either
-            };
-
             if (rows <= kSmallRows) {
                 // ------------------------------------------------ short tile
                 // The tile's rows lie in every quarter of the lanes, and the warp of a
@@ -674,6 +683,73 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 const int itk = ir >> a.gshift;
                 const size_t th = (size_t)(s.tok0 + itk) * a.Hq + (size_t)s.g * a.G + (ir & (a.G - 1));
                 float mi = kNegInf, li = 0.f, inv = 1.f;
+                bool searched = false;
+                uint32_t *kinds = sm.kinds[joint ? 0 : x];
+                // The kinds of non-finite values that all rows see, by all threads, 16 bytes of a
+                // key each: 1 to 2 us per unit, so that 5 * 10^7 keys of one segment stay within
+                // the limit of the other warps' waits (a thread per row and column, key after
+                // key: 0.27 us per key and pass).
+                auto search = [&]() {
+                    constexpr int CH = D / 8;
+                    const int lots = (joint ? kSoftmax : 128) / CH, cc = it % CH, at = it / CH;
+                    const int *pre_list = a.prefix_table + (size_t)s.group * a.max_prefix_pages;
+                    const int *own_list = a.table + (size_t)s.row * a.max_pages;
+                    if (it < CH) kinds[it] = 0;
+                    meet();
+                    uint32_t found = 0;
+#pragma unroll 1
+                    for (int u = k0; u < k0 + n; ++u) {
+                        const int *list = u < pu ? pre_list : own_list;
+                        const int key0 = (u < pu ? u : u - pu) * kUnitKeys;
+                        const int end = min(u < pu ? pre_keys : min(s.base + 1, keys), key0 + kUnitKeys);
+#pragma unroll 1
+                        for (int key = key0 + at; key < end; key += 4 * lots) {
+                            uint4 y[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int k = key + e * lots, id = k < end ? list[k >> a.shift] : -1;
+                                y[e] = make_uint4(0, 0, 0, 0);
+                                if (id >= 0 && id < a.n_pages)
+                                    y[e] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.v_pages) +
+                                        ((((long long)id * a.Hkv + s.g) << a.shift) + (k & (a.S - 1))) * D + 8 * cc);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) found |= non_finite(y[e]);
+                        }
+                    }
+                    if (found) atomicOr(&kinds[cc], found);
+                    meet();
+                };
+                // o[i]: the sum of the non-finite values, if there are any, of column c + i over
+                // the segment's keys that a row with `own` local keys sees
+                auto sum_non_finite = [&](int own, int c, float (&o)[4]) {
+                    const uint32_t w = kinds[c >> 3] >> (c & 7);
+                    float t[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        t[i] = ((w >> i) & 1u ? -kNegInf : 0.f) + ((w >> (8 + i)) & 1u ? kNegInf : 0.f) +
+                               ((w >> (16 + i)) & 1u ? __int_as_float(0x7fffffff) : 0.f);
+#pragma unroll 1
+                    for (int f = 0; fixed && f < kFixUnits * 4; ++f) {
+                        uint32_t bits = fix[f >> 2][f & 3];
+                        while (bits) {
+                            const int key = (masked - pu) * kUnitKeys + 32 * f + __ffs(bits) - 1;
+                            bits &= bits - 1;
+                            if (key >= own) continue;
+                            const int id = a.table[(size_t)s.row * a.max_pages + (key >> a.shift)];
+                            if (id < 0 || id >= a.n_pages) continue;
+                            float y[4];
+                            load_vec<__nv_bfloat16, 4>(static_cast<const __nv_bfloat16 *>(a.v_pages) +
+                                ((((long long)id * a.Hkv + s.g) << a.shift) + (key & (a.S - 1))) * D + c, y);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (!(y[i] - y[i] == 0.f)) t[i] += y[i];
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (t[i] != 0.f) o[i] = t[i];   // a NaN is not 0 either
+                };
                 for (int c0 = 0; c0 < D; c0 += cols) {
 #pragma unroll 1
                     for (int c = c0; c < c0 + cols; c += 16) {
@@ -690,6 +766,8 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                         }
                     }
                     meet();
+                    float o[4] = {0.f, 0.f, 0.f, 0.f};
+                    bool odd = false;
                     if (ir < rows) {
                         if (c0 == 0) {
 #pragma unroll
@@ -701,7 +779,6 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                                 }
                             if (s.direct) inv = li == 0.f ? 0.f : 1.f / li;
                         }
-                        float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                         for (int w = 0; w < 8; ++w)
                             if (w >= w_lo && w < w_hi) {
@@ -712,7 +789,16 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                         // quarters (0 times infinity is not a number).  The sum of the ones
                         // the row sees is the result; a NaN among the scores is in l already.
                         const float bad = (o[0] - o[0]) + (o[1] - o[1]) + (o[2] - o[2]) + (o[3] - o[3]);
-                        if ((fixed || bad != 0.f) && li == li) sum_non_finite(min(s.base + itk + 1, keys), c0 + ic, o);
+                        odd = (fixed || bad != 0.f) && li == li;
+                    }
+                    // all have read the warps' outputs
+                    if (joint ? softmax_any(odd) : stream_any(x, odd)) {
+                        if (!searched) search();
+                        searched = true;
+                        if (odd) sum_non_finite(min(s.base + itk + 1, keys), c0 + ic, o);
+                        meet();
+                    }
+                    if (ir < rows) {
                         if (s.direct) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i) o[i] *= inv;
@@ -722,7 +808,6 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                                 make_float4(o[0], o[1], o[2], o[3]);
                         }
                     }
-                    meet();
                 }
                 if (ir < rows && ic == 0) {
                     if (!s.direct) a.ws_ml[s.prow + ir] = make_float2(mi, li);

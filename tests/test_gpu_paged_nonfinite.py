@@ -60,3 +60,54 @@ def test_scores_of_minus_infinity_alone(dt, tok):
     even = torch.arange(R * tok) % 2 == 0
     assert torch.isnan(o[even]).all() and not torch.isfinite(z[even]).any()
     assert (o[~even] == 0).all() and (z[~even] == -math.inf).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_infinite_values_in_a_very_long_key_list(d):
+    """296 prefixes of 1.6 million keys (1024 keys of 8 pages, over and over), 32 query rows each, two whole
+    lists per SM: infinite and NaN values in 8 places spread over the columns are found in time
+    (the other warps' waits have a limit of about a second), and a value that only the last token of a row sees
+    reaches it alone."""
+    R, tok, G, S, reps = 296, 4, 8, 128, 1600
+    b = Batch("bf16", G, 1, d, S, new=[tok] * R, seq=[tok] * R, goff=list(range(R + 1)), pre=[1024] * R, seed=33)
+    pages = torch.as_tensor(b.ptable[0, :8])
+    b.ptable = pages.repeat(reps).expand(R, 8 * reps).numpy().copy()
+    b.pre = [1024 * reps] * R
+    b.dev["prefix_table"] = torch.as_tensor(b.ptable, dtype=torch.int32).cuda()
+    vals = torch.zeros(d)                  # what each column's sum becomes
+    for i in range(8):
+        c = i * (d // 8) + 3
+        vals[c] = [math.inf, -math.inf, math.nan, math.inf][i % 4]
+        b.vd[int(pages[i]), 0, 17 * i, c] = vals[c]
+        if i == 7:                         # both signs: no number
+            b.vd[int(pages[2]), 0, 1, c] = -math.inf
+            vals[c] = math.nan
+    last = int(b.table[5, 0])
+    b.vd[last, 0, tok - 1, 0] = -math.inf  # the last token of row 5
+    out, lse = b.run()
+    o, z = out.cpu().double(), lse.cpu().double()
+    t5 = 5 * tok + tok - 1
+    assert (o[t5, :, 0] == -math.inf).all()
+    o[t5, :, 0] = 0
+    for c in range(d):
+        if vals[c] != 0:
+            assert (torch.isnan(o[..., c]).all() if math.isnan(vals[c]) else (o[..., c] == vals[c]).all()), c
+            o[..., c] = 0
+    assert torch.isfinite(o).all() and torch.isfinite(z).all()
+    # rows 4 to 6 against the formula: the prefix's keys count `reps` times
+    kp, vp = b.kd.cpu(), b.vd.cpu().nan_to_num(0, 0, 0)
+    rows = slice(4, 7)
+    q, tab = b.q[4 * tok:7 * tok], b.table[rows]
+    off = [0, tok, 2 * tok, 3 * tok]
+    base = b.ptable[rows, :8]
+    po, pl, pa, pd, _ = C.attention(q, kp, vp, tab, off, [0] * 3, b.scale, [0, 1, 2, 3], [1024] * 3, base)
+    lo, ll, la, ld, _ = C.attention(q, kp, vp, tab, off, [tok] * 3, b.scale)
+    pl = pl + math.log(reps)
+    rl = torch.logaddexp(pl, ll)
+    wp, wl = torch.exp(pl - rl)[..., None], torch.exp(ll - rl)[..., None]
+    ref, a = wp * po + wl * lo, wp * pa + wl * la
+    keep = vals == 0
+    cnt = torch.full((3 * tok,), 1024 * reps + tok)
+    eo, ez = C.attention_bounds(ref, rl, a, torch.maximum(pd, ld), cnt, d, b.dt)
+    got, gz = o[4 * tok:7 * tok], z[4 * tok:7 * tok]
+    assert ((got - ref)[..., keep].abs() <= eo[..., keep])[..., 1:].all() and ((gz - rl).abs() <= ez).all()
