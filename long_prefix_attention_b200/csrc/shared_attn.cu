@@ -228,7 +228,7 @@ __device__ void run_few(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
                 if (tx == 0) sm.al[hw] = al;
             }
             __syncthreads();
-            // a weight of 0 at a key the row does not see must not meet its value
+            // the weight of 0 of a key that a row does not see must not meet its value
             const bool masked = !f.pre && f.kb + kKB > own_first;
 #pragma unroll
             for (int r = 0; r < kFew; ++r) {
@@ -239,6 +239,7 @@ __device__ void run_few(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
 #pragma unroll 2
             for (int i = 0; i < kKB / 16; ++i) {
                 const int kk = hw * (kKB / 16) + i;
+                const int hidden = masked ? (f.kb + kk - s.t.base) * a.G : 0;   // rows that do not see this key
                 float4 vx[NC];
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
@@ -249,7 +250,7 @@ __device__ void run_few(const AttnArgs &a, const Seg &s, Smem<D> &sm) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float w = e == 0 ? w4.x : e == 1 ? w4.y : e == 2 ? w4.z : w4.w;
-                        if (masked && w == 0.f) continue;
+                        if (r + e < hidden) continue;
 #pragma unroll
                         for (int c = 0; c < NC; ++c) axpy4(w, vx[c], o[r + e][c]);
                     }
@@ -375,8 +376,8 @@ __device__ void run_rows(const AttnArgs &a, const Seg &s, Smem<D> &sm, int rb) {
 #pragma unroll
                     for (int i = 0; i < MR; ++i) {
                         const float p = e == 0 ? px[i].x : e == 1 ? px[i].y : e == 2 ? px[i].z : px[i].w;
-                        // a weight of 0 at a key the row does not see must not meet its value
-                        if (masked && p == 0.f) continue;
+                        // the weight of 0 of a key that the row does not see must not meet its value
+                        if (masked && kb + k + e >= (pre ? k1 : own[i])) continue;
                         axpy4(p, vx, o[i][c]);
                     }
                 }

@@ -759,7 +759,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                         if (live) {
                             float *e = &sm.ex[warp][(lane << csh) + c - c0];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = w_own == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * w_own);
+                            for (int i = 0; i < 16; ++i) o[i] = m_used == kNegInf ? 0u : __float_as_uint(__uint_as_float(o[i]) * w_own);
 #pragma unroll
                             for (int i = 0; i < 16; i += 4)
                                 *reinterpret_cast<uint4 *>(e + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
@@ -918,8 +918,11 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                 // the states of a small tile's streams, joined
                 float w0 = 1.f, w1 = 0.f, m = m_used;
                 const bool two = joint && !dual;
+                bool none0 = false, none1 = false;
                 if (two) {
                     const float2 s0 = sm.ml[0][row], s1 = sm.ml[1][row];
+                    none0 = s0.x == kNegInf;
+                    none1 = s1.x == kNegInf;
                     m = max_nan(s0.x, s1.x);
                     const float ref = m == kNegInf ? 0.f : m;
                     w0 = ex2f(s0.x - ref);
@@ -942,8 +945,8 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                         // a stream that saw no key of the row holds no value for it
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            const float u0 = w0 == 0.f ? 0.f : __uint_as_float(o[i]) * w0;
-                            o[i] = __float_as_uint(w1 == 0.f ? u0 : fmaf(__uint_as_float(o1[i]), w1, u0));
+                            const float u0 = none0 ? 0.f : __uint_as_float(o[i]) * w0;
+                            o[i] = __float_as_uint(none1 ? u0 : fmaf(__uint_as_float(o1[i]), w1, u0));
                         }
                     } else {
                         tmem_wait_ld();

@@ -111,3 +111,40 @@ def test_infinite_values_in_a_very_long_key_list(d):
     eo, ez = C.attention_bounds(ref, rl, a, torch.maximum(pd, ld), cnt, d, b.dt)
     got, gz = o[4 * tok:7 * tok], z[4 * tok:7 * tok]
     assert ((got - ref)[..., keep].abs() <= eo[..., keep])[..., 1:].all() and ((gz - rl).abs() <= ez).all()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("tok", [1, 6, 40, 100])
+@pytest.mark.parametrize("low", [32, 128])
+def test_an_infinite_value_behind_a_weight_that_underflows(dt, tok, low):
+    """Scores of -225 against others near 0: the weight is 0 in fp32, but the key is seen, and
+    e^-225 times infinity is not finite, wherever the key lies and whatever shares its tile:
+    alone among others, or in a run of `low` such keys (a warp's share of a unit, or a
+    whole unit).  Columns and rows without such a value keep their results."""
+    R = 32
+    b = Batch(dt, 16, 8, 64, 32, new=[tok] * R, seq=[tok + 200] * R, goff=list(range(R + 1)), pre=[428] * R, seed=34)
+    b.q[..., 0] = 30.0
+    b.kd[..., 0] = 0.0
+    places, odd = [], torch.arange(R * tok) // tok % 2 == 1
+    for r in range(R):
+        for i in range(4, 4 + low // 32):                                    # keys 128 .. 128 + low of the prefix
+            b.kd[int(b.ptable[r, i]), :, :, 0] = -60.0
+        places += [(int(b.ptable[r, 4]), 8, 33)]
+        if r % 2 == 0:      # prefix keys 7 and 426, local keys 5 and 200, the first new one
+            places += [(int(b.ptable[r, 0]), 7, 3), (int(b.ptable[r, 13]), 10, 11), (int(b.table[r, 0]), 5, 17),
+                       (int(b.table[r, 6]), 8, 25)]
+    for page, at, col in places:
+        b.kd[page, :, at, 0] = -60.0
+    clean, clse = b.run()
+    for page, at, col in places:
+        b.vd[page, :, at, col] = math.inf
+    out, lse = b.run()
+    assert torch.equal(lse, clse)
+    finite, same = torch.isfinite(out).cpu(), (out == clean).cpu()
+    assert not finite[..., 33].any().item()
+    assert not finite[~odd][..., [3, 11, 17, 25]].any().item()
+    keep = torch.ones(64, dtype=torch.bool)
+    keep[33] = False
+    assert same[odd][..., keep].all().item()
+    keep[[3, 11, 17, 25]] = False
+    assert same[..., keep].all().item()
