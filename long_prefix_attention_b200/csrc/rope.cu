@@ -6,10 +6,11 @@
 //   (a, b) -> m (a cos - b sin, b cos + a sin);   inverse: sin -> -sin,
 // which is the transpose of the rotation, hence its gradient.
 //
-// The angle is reduced exactly: f_i / (2 pi), a 64-bit float, becomes a
+// The angle is reduced exactly: f_i / (2 pi), a product of two words, becomes a
 // fraction of a turn in 64-bit fixed point, and p times it modulo 2^64 is the
-// fraction of the turn whatever p is (error p 2^-64 turns and the 2^-53
-// relative one of f_i, 3e-10 rad at p = 10^6).  Its top two bits (rounded)
+// fraction of the turn whatever p is (error p 2^-64 turns; with the product in one
+// fp64 word 3.5e-8 turns at p = 2^31).  Its top 32 bits (rounded) are kept, within
+// 2^-32 turns in all; the top two of them (rounded)
 // pick the quarter; the rest, at most an eighth of a turn, loses nothing that
 // fp32 holds.  bf16 outputs take the hardware sine and cosine there (absolute
 // error 2^-21, far below the 2^-9 of the rounding); fp32 ones sincospif.
@@ -51,14 +52,17 @@ struct Args {
 
 // fraction of a turn per position, modulo 1, in units of 2^-64
 __device__ __forceinline__ unsigned long long turns(double f) {
-    double t = f * 0.15915494309189535;  // 1 / (2 pi)
+    constexpr double c0 = 0x1.45f306dc9c883p-3, c1 = -0x1.6b01ec5417056p-57;  // 1 / (2 pi) in two words
+    double t = f * c0, e = fma(f, c0, -t) + f * c1;
     t -= rint(t);
-    return t >= 0.5 ? 0x8000000000000000ull : (unsigned long long)__double2ll_rn(t * 18446744073709551616.0);
+    e -= rint(e);
+    const unsigned long long hi = t >= 0.5 ? 0x8000000000000000ull : (unsigned long long)__double2ll_rn(t * 18446744073709551616.0);
+    return hi + (unsigned long long)__double2ll_rn(e * 18446744073709551616.0);
 }
 
 template <bool FAST>
 __device__ __forceinline__ void cos_sin(unsigned long long turn, int p, float ms, float sgn, float &c, float &s) {
-    const unsigned f = (unsigned)((turn * (unsigned long long)(long long)p) >> 32);
+    const unsigned f = (unsigned)((turn * (unsigned long long)(long long)p + 0x80000000ull) >> 32);
     const unsigned quarter = (f + 0x20000000u) >> 30;
     const float r = (float)(int)(f - (quarter << 30));  // within an eighth of a turn, units 2^-32
     float sn, cs;
