@@ -590,8 +590,9 @@ asm_status asm_rope(const void *x, int64_t x_st, int64_t x_sh, int T, int H,
  * caches at the tokens' slots.  Tokens whose slot lies outside
  * [0, n_pages x page_size) store nothing (q is still turned).  Two tokens must
  * not have the same slot.  q, k, v are strided as in asm_rope (views of one
- * packed projection, for example); q_out may be q.  The caches must not
- * overlap the other arrays.  One launch.
+ * packed projection, for example); q_out may be q and must not overlap any other
+ * array.  The caches must not overlap the other arrays (ASM_ERR_INVALID_ARG where
+ * one lies between the first and the last element of another).  One launch.
  */
 asm_status asm_rope_append(const void *q, int64_t q_st, int64_t q_sh,
                            const void *k, int64_t k_st, int64_t k_sh,
@@ -613,7 +614,8 @@ asm_status asm_rope_append(const void *q, int64_t q_st, int64_t q_sh,
  *   prefix_len [NG]  tokens of each prefix
  * Offsets that fall are raised to the largest before them, offsets and
  * lengths beyond T, R, the tables' pages are clamped.
- *   plan       asm_shared_plan_size(R, NG, T, Hq, Hkv) bytes (any content)
+ *   plan       asm_shared_plan_size(R, NG, T, Hq, Hkv) bytes (any content),
+ *              none of the inputs within (ASM_ERR_INVALID_ARG)
  * NG <= 4096, T <= 2^24; page_size x max_pages and page_size x
  * max_prefix_pages at most 2^30 (ASM_ERR_INVALID_ARG).  The plan belongs to these
  * sizes and to the device it was made on; any number of calls may read it.  Work
@@ -634,7 +636,7 @@ asm_status asm_shared_plan(const int32_t *q_off, const int32_t *seq_len,
  * 0 .. seq_len[r] - n + i.  A prefix is read once for all the rows that share
  * it (per 256 query rows of a KV head), in contrast to asm_flash_decode for
  * any number of prefixes, new tokens per row and pages.
- *   q, out       [T, Hq, d] dt (out must not overlap q)
+ *   q, out       [T, Hq, d] dt
  *   k_pages, v_pages [n_pages, Hkv, S, d] dt (the new tokens' included)
  *   table        [R, max_pages] int32, prefix_table [NG, max_prefix_pages]
  *   lse_out      [T, Hq] fp32 (natural log), or NULL
@@ -643,6 +645,8 @@ asm_status asm_shared_plan(const int32_t *q_off, const int32_t *seq_len,
  *   ws           asm_shared_attention_workspace_size(...) bytes, word 0 zeroed
  *                once (asm_workspace_init); asm_workspace_error reads it.  It
  *                grows with T x Hq (partial states of the rows)
+ * out, lse_out and ws must overlap neither an input nor one another
+ * (ASM_ERR_INVALID_ARG).
  * A token without any key, or whose scores are all -inf, gets (0, -inf); a
  * score of +inf gives NaN, as in the formula.  Tokens outside every row are
  * left as they were.  Keys that a token does not see (later tokens, places behind a

@@ -463,6 +463,14 @@ asm_status asm_rope_append(const void *q, int64_t q_st, int64_t q_sh, const void
     if (q == q_out && ((T > 1 && q_st != o_st) || (Hq > 1 && q_sh != o_sh))) return ASM_ERR_INVALID_ARG;
     const size_t cache = (size_t)n_pages * page_size * Hkv * d * es;
     if (overlap(k_pages, cache, v_pages, cache)) return ASM_ERR_INVALID_ARG;
+    // from the first to the last element of a view
+    const auto span = [&](int64_t st, int64_t sh, int H) { return ((size_t)(T - 1) * st + (size_t)(H - 1) * sh + d) * es; };
+    const void *other[7] = {q, k, v, q_out, pos, slot, freq};
+    const size_t other_n[7] = {span(q_st, q_sh, Hq), span(k_st, k_sh, Hkv), span(v_st, v_sh, Hkv), span(o_st, o_sh, Hq),
+                               4 * (size_t)T, 4 * (size_t)T, 8 * (size_t)(rot / 2)};
+    for (int i = 0; i < 7; ++i)
+        if (overlap(other[i], other_n[i], k_pages, cache) || overlap(other[i], other_n[i], v_pages, cache))
+            return ASM_ERR_INVALID_ARG;
     return cuda_status(asm_rope_append_launch(q, q_st, q_sh, k, k_st, k_sh, v, v_st, v_sh, T, Hq, Hkv, d, dt, pos,
                                               slot, freq, rot, (int)layout, mscale, q_out, o_st, o_sh, k_pages,
                                               v_pages, n_pages, page_size, num_sms(), stream));
@@ -493,7 +501,11 @@ asm_status asm_shared_plan(const int32_t *q_off, const int32_t *seq_len, const i
         return ASM_ERR_INVALID_ARG;
     if (!aligned(q_off, 4) || !aligned(seq_len, 4)) return ASM_ERR_INVALID_ARG;
     if (NG > 0 && (!aligned(group_off, 4) || !aligned(prefix_len, 4))) return ASM_ERR_INVALID_ARG;
-    if (!aligned(plan, 16) || plan_bytes < asm_shared_plan_bytes(R, NG, T, Hq, Hkv)) return ASM_ERR_WORKSPACE;
+    const size_t need = asm_shared_plan_bytes(R, NG, T, Hq, Hkv);
+    if (!aligned(plan, 16) || plan_bytes < need) return ASM_ERR_WORKSPACE;
+    if (overlap(plan, need, q_off, 4 * ((size_t)R + 1)) || overlap(plan, need, seq_len, 4 * (size_t)R) ||
+        (NG > 0 && (overlap(plan, need, group_off, 4 * ((size_t)NG + 1)) || overlap(plan, need, prefix_len, 4 * (size_t)NG))))
+        return ASM_ERR_INVALID_ARG;
     return cuda_status(asm_shared_plan_launch(q_off, seq_len, group_off, prefix_len, R, NG, T, Hq, Hkv, page_size,
                                               max_pages, NG > 0 ? max_prefix_pages : 0, plan, num_sms(), stream));
 }
@@ -518,10 +530,23 @@ asm_status asm_shared_attention(const void *q, const void *k_pages, const void *
     if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(table, 4) || !aligned(out, 16))
         return ASM_ERR_INVALID_ARG;
     if ((NG > 0 && !aligned(prefix_table, 4)) || (lse_out && !aligned(lse_out, 4))) return ASM_ERR_INVALID_ARG;
-    if (!aligned(plan, 16) || plan_bytes < asm_shared_plan_bytes(R, NG, T, Hq, Hkv)) return ASM_ERR_WORKSPACE;
-    if (!aligned(ws, 16) || ws_bytes < asm_shared_attention_ws_bytes(T, Hq, d, num_sms())) return ASM_ERR_WORKSPACE;
-    const size_t bytes = (size_t)T * Hq * d * (dt == ASM_BF16 ? 2 : 4);
-    if (overlap(q, bytes, out, bytes)) return ASM_ERR_INVALID_ARG;  // a tile's queries are read several times
+    const size_t plan_need = asm_shared_plan_bytes(R, NG, T, Hq, Hkv), ws_need = asm_shared_attention_ws_bytes(T, Hq, d, num_sms());
+    if (!aligned(plan, 16) || plan_bytes < plan_need) return ASM_ERR_WORKSPACE;
+    if (!aligned(ws, 16) || ws_bytes < ws_need) return ASM_ERR_WORKSPACE;
+    // inputs are read while outputs and partial states are written: no output within
+    // an input or another output
+    const size_t es = dt == ASM_BF16 ? 2 : 4, bytes = (size_t)T * Hq * d * es, cache = (size_t)n_pages * Hkv * page_size * d * es;
+    const void *wr[3] = {out, lse_out, ws};
+    const size_t wr_n[3] = {bytes, lse_out ? 4 * (size_t)T * Hq : 0, ws_need};
+    const void *rd[6] = {q, k_pages, v_pages, table, prefix_table, plan};
+    const size_t rd_n[6] = {bytes, cache, cache, 4 * (size_t)R * max_pages, NG > 0 ? 4 * (size_t)NG * max_prefix_pages : 0,
+                            plan_need};
+    for (int o = 0; o < 3; ++o) {
+        for (int i = 0; i < 6; ++i)
+            if (overlap(wr[o], wr_n[o], rd[i], rd_n[i])) return ASM_ERR_INVALID_ARG;
+        for (int i = 0; i < o; ++i)
+            if (overlap(wr[o], wr_n[o], wr[i], wr_n[i])) return ASM_ERR_INVALID_ARG;
+    }
     return cuda_status(asm_shared_attention_launch(q, k_pages, v_pages, n_pages, page_size, table, max_pages,
                                                    prefix_table, NG > 0 ? max_prefix_pages : 0, plan, R, NG, T, Hq,
                                                    Hkv, d, scale, dt, out, lse_out, ws, num_sms(), stream));

@@ -247,3 +247,26 @@ def test_the_quintic_exponential():
     bits = (p.view(np.uint32) + (y.view(np.uint32) << np.uint32(23))).astype(np.uint32)
     got, ref = bits.view(f32).astype(np.float64), np.exp2(t.astype(np.float64))
     assert (np.abs(got - ref) / ref).max() < 2.0 ** -20 / 2
+
+
+def test_shared_attention_refuses_outputs_within_other_arrays(lib):
+    """Tiles of a call read their inputs and the partial states while others write."""
+    ws = lib.asm_shared_attention_workspace_size(100, 8, 2, 128)
+    pl = lib.asm_shared_plan_size(4, 2, 100, 8, 2)
+    out_n, lse_n, kv_n = 100 * 8 * 128 * 2, 100 * 8 * 4, 64 * 2 * 16 * 128 * 2
+    for kw in (dict(out=at(1)), dict(out=at(2, kv_n - 16)), dict(out=at(3)), dict(out=at(4, 48)), dict(out=at(5, pl - 16)),
+               dict(out=at(8)), dict(lse=at(0)), dict(lse=at(1, 64)), dict(lse=at(2)), dict(lse=at(3, 4)), dict(lse=at(4)),
+               dict(lse=at(5)), dict(lse=at(6)), dict(lse=at(6, out_n - 4)), dict(lse=at(8, 256)), dict(ws=at(0)),
+               dict(ws=at(1, 16)), dict(ws=at(2)), dict(ws=at(3)), dict(ws=at(4)), dict(ws=at(5)), dict(ws=at(6)),
+               dict(ws=at(7)), dict(out=at(9), ws=at(9, out_n - 16)), dict(out=at(9), lse=at(9, out_n - 4))):
+        assert attn(lib, **kw) == INVALID, {k: hex(v.value) for k, v in kw.items()}
+    for kw in (dict(qo=at(4)), dict(sl=at(4, 256)), dict(go=at(4, pl - 16)), dict(pl=at(4, 512)), dict(plan=at(1))):
+        assert plan(lib, **kw) == INVALID, kw
+    assert lse_n and ws
+
+
+def test_rope_append_refuses_caches_within_other_arrays(lib):
+    cache = 4 * 16 * 2 * 128 * 2
+    for kw in (dict(q=at(7)), dict(k=at(7, 256)), dict(v=at(8, cache - 2)), dict(qo=at(8)), dict(pos=at(7)), dict(slot=at(8, 4)),
+               dict(f=at(7, 64)), dict(kp=at(1, 2 * 4 * 256)), dict(vp=at(2, 256))):
+        assert append(lib, **kw) == INVALID, kw
