@@ -270,3 +270,43 @@ def test_rope_append_refuses_caches_within_other_arrays(lib):
     for kw in (dict(q=at(7)), dict(k=at(7, 256)), dict(v=at(8, cache - 2)), dict(qo=at(8)), dict(pos=at(7)), dict(slot=at(8, 4)),
                dict(f=at(7, 64)), dict(kp=at(1, 2 * 4 * 256)), dict(vp=at(2, 256))):
         assert append(lib, **kw) == INVALID, kw
+
+
+def tiles_provided(plan_bytes, T):
+    """Tiles of 64 bytes between the workers' first tiles (256 + 4096 bytes) and the token map
+    (8 bytes a token, 256-byte aligned) of a plan of that size."""
+    return ((plan_bytes - 8 * T) // 256 * 256 - 4352) // 64
+
+
+def partial_rows_provided(ws_bytes, d):
+    """Partial rows (two floats of statistics, d of output) that surely fit a workspace of
+    that size, its error word and two alignments apart."""
+    return (ws_bytes - 256 - 2 * 255) // (8 + 4 * d)
+
+
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+def test_the_size_functions_cover_the_plan(lib, G):
+    """For random lengths, the tiles of the plan and the rows of its partial states fit what
+    asm_shared_plan_size and asm_shared_attention_workspace_size return."""
+    import random
+    rng = random.Random(50 + G)
+    Hkv, workers = 4, 148               # without a GPU the library sizes for 148 multiprocessors
+    Hq = G * Hkv
+    tightest = 0.0
+    for _ in range(300):
+        R, NG = rng.randint(1, 60), rng.randint(0, 4)
+        new = [rng.choice([0, 1, 1, 3, rng.randint(0, 900), 128 // G, 128 // G + 1]) for _ in range(R)]
+        old = [rng.choice([0, 100, 9000]) for _ in range(R)]
+        pre = [rng.choice([0, 1, 300, 40000]) for _ in range(NG)]
+        cuts = sorted(rng.randint(0, R) for _ in range(NG + 1))
+        T = max(1, sum(new))
+        tiles = plan_tiles(new, old, pre, cuts, G)
+        have = tiles_provided(lib.asm_shared_plan_size(R, NG, T, Hq, Hkv), T)
+        assert len(tiles) <= have
+        tightest = max(tightest, len(tiles) / have)
+        cost = [(4 if r > 128 else 2) * (u + 1) if u else 0 for r, u in tiles]
+        size = max(C.cdiv(Hkv * sum(cost), workers), 4 if any(r > 128 for r, _ in tiles) else 2)
+        need = sum((c // size + 2) * Hkv * r for (r, u), c in zip(tiles, cost) if u)
+        for d in (64, 128):
+            assert need <= partial_rows_provided(lib.asm_shared_attention_workspace_size(T, Hq, Hkv, d), d)
+    assert tightest > 0.3               # the bound is not checked against thin air
