@@ -10,9 +10,8 @@
 // fraction of a turn in 64-bit fixed point, and p times it modulo 2^64 is the
 // fraction of the turn whatever p is (error p 2^-64 turns; with the product in one
 // fp64 word 3.5e-8 turns at p = 2^31).  Its top 32 bits (rounded) are kept, within
-// 2^-32 turns in all; the top two of them (rounded)
-// pick the quarter; the rest, at most an eighth of a turn, loses nothing that
-// fp32 holds.  bf16 outputs take the hardware sine and cosine there (absolute
+// 2^-32 turns in all; the top two of them (rounded) pick the quarter; the rest, at
+// most an eighth of a turn, loses nothing that fp32 holds.  bf16 outputs take the hardware sine and cosine there (absolute
 // error 2^-21, far below the 2^-9 of the rounding); fp32 ones sincospif.
 //
 // Bound by memory: one read and one write of every element.  A thread keeps
@@ -265,11 +264,13 @@ cudaError_t launch(const Args &a, int num_sms, cudaStream_t st) {
         return cudaGetLastError();
     }
     const int units = a.d / (2 * N);
-    // Slices per token: enough to cover the card when there are few tokens
-    // (each slice forms the sines again), otherwise one warp's worth.
+    // Slices per token: one warp's worth, twice as many while that leaves fewer than 128
+    // threads per SM (each slice forms the sines again).  Queries of 32 heads, bf16, one
+    // warp's worth against the rule: 64 tokens 4.4 us against 3.2, 512 4.7 against 4.0, 1024
+    // 4.9 either way; a bound of 2048 threads 6.2 and 10.1 for 512 and 1024.
     int slices = 32 / units;
     while (slices > 1 && slices > a.H) slices /= 2;
-    while ((long long)a.T * slices * units < 2048LL * num_sms && 2 * slices * units <= kThreads && slices < a.H)
+    while ((long long)a.T * slices * units < 128LL * num_sms && 2 * slices * units <= kThreads && slices < a.H)
         slices *= 2;
     const int toks = kThreads / (units * slices);
     const long long blocks = ((long long)a.T + toks - 1) / toks;
