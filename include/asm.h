@@ -523,7 +523,8 @@ asm_status asm_decode_step_search(const void *q, const void *q_search,
  * it is refused if its tokens end past T, if its table is too short, or if
  * the pages asked for by the rows up to it exceed the free ones; pages
  * returned by this step serve the next one.  A refused row keeps its length
- * and pages, its tokens get slot -1.  Lengths below 0 or above the table are
+ * and pages, its tokens keep their places in the batch and get slot -1 (what
+ * the step's attention writes for them means nothing).  Lengths below 0 or above the table are
  * clamped.  The step's inputs are not changed (the ring and the table only
  * where nothing is read), so outputs may not be the inputs: feed seq_len and
  * pool_out to the next call.  No workspace; one launch.
@@ -633,9 +634,12 @@ asm_status asm_shared_plan(const int32_t *q_off, const int32_t *seq_len,
  * asm_shared_attention -- attention of the batch's new tokens over the prefix
  * of their row's group and over the row's own tokens up to themselves: the new
  * token i of n of row r sees the whole prefix and the local keys
- * 0 .. seq_len[r] - n + i.  A prefix is read once for all the rows that share
- * it (per 256 query rows of a KV head), in contrast to asm_flash_decode for
- * any number of prefixes, new tokens per row and pages.
+ * 0 .. seq_len[r] - n + i.  A prefix is read once for neighbouring rows that
+ * share it (per 256 query rows of a KV head).  A row with more than 128 query
+ * rows of a KV head (tokens x Hq / Hkv) reads it for itself, and parts the rows
+ * before it from those behind: rows sorted by their new tokens read less.  In
+ * contrast to asm_flash_decode for any number of prefixes, new tokens per row
+ * and pages.
  *   q, out       [T, Hq, d] dt
  *   k_pages, v_pages [n_pages, Hkv, S, d] dt (the new tokens' included)
  *   table        [R, max_pages] int32, prefix_table [NG, max_prefix_pages]
@@ -655,9 +659,9 @@ asm_status asm_shared_plan(const int32_t *q_off, const int32_t *seq_len,
  * column infinite or NaN, however small the key's weight (short tiles search
  * for them once more, which costs about 2 us per 128 keys).  A page id outside
  * [0, n_pages) reads as zeros and sets the error word to ASM_ERR_INVALID_ARG,
- * and so does a plan of other sizes, with which the call writes nothing; a device-side wait that gives up sets
- * ASM_ERR_TIMEOUT (outputs not valid).  (out, lse_out) is an attention state:
- * with asm_decode_step over no local tokens and asm_merge_states it joins the
+ * and so does a plan of other sizes, with which the call writes nothing; a
+ * device-side wait that gives up sets ASM_ERR_TIMEOUT (outputs not valid).
+ * (out, lse_out) is an attention state: with asm_decode_step over no local tokens and asm_merge_states it joins the
  * memory's retrieved state in place of an explicit prefix.
  * bf16 runs on the tcgen05 tensor cores (bf16 products and weights, fp32
  * accumulators, statistics and joins), fp32 on CUDA cores.  Two launches, with
@@ -682,9 +686,10 @@ asm_status asm_shared_attention(const void *q, const void *k_pages,
 asm_status asm_workspace_init(void *ws, size_t ws_bytes, cudaStream_t stream);
 
 /*
- * asm_wait_spin_limit -- how many unsuccessful mbarrier try_wait polls any
+ * asm_wait_spin_limit -- how many unsuccessful mbarrier try_wait polls a
  * wait in the library's kernels makes before it gives up, sets the error
- * word to ASM_ERR_TIMEOUT and lets its CTA finish.
+ * word to ASM_ERR_TIMEOUT and lets its CTA finish; 64 times as many, about
+ * the same time, where a single lane waits in asm_shared_attention.
  */
 uint32_t asm_wait_spin_limit(void);
 

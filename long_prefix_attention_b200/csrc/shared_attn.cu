@@ -31,10 +31,14 @@ namespace shared {
 // whole 16 x D output, summed over the half-warps at the end; so K and V leave
 // shared memory once per half (64 rows of 2048 local keys: 139 us, a row-wise
 // split that waits for its loads 190).  Longer tiles take 32, 48 or 64 rows at a
-// time, 2, 3 or 4 rows x 4 keys of scores a thread, which is bound by the FMA
-// pipe (always 64: 279 us against 251 for 20 rows of a group behind 20000 keys,
-// 49 against 43 for 44 query rows behind 4000); 17 to 64 rows through the short
-// path in turns of 16 measured slower (44 rows: 64 us).
+// time, 2, 3 or 4 rows x 4 keys of scores a thread (always 64: 279 us against 251
+// for 20 rows of a group behind 20000 keys, 49 against 43 for 44 query rows behind
+// 4000); 17 to 64 rows through the short path in turns of 16 measured slower (44
+// rows: 64 us).  Neither form reaches the FMA rate: a thread loads 4 + MR words of 16
+// bytes from shared memory for 16 MR FMAs of the scores, and waits at barriers.
+// 44 query rows behind two 4000-key prefixes: 43 us, the FMA pipe 12% busy, the SMs
+// half of the time, since 172 units of 128 keys meet 148 SMs; 1447 tokens of four
+// chunks behind 4000 keys 937 us, 36% of the FMA rate.
 
 __device__ __forceinline__ float dot4(const float4 &x, const float4 &y, float t) {
     t = fmaf(x.x, y.x, t);
@@ -576,7 +580,9 @@ cudaError_t launch_merge(const AttnArgs &a, int num_sms, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     // Few pairs have many states each (their keys are split further): eight
-    // warps a pair while the pairs leave most of the card empty, else one.
+    // warps a pair while the pairs leave most of the card empty, else one.  Decode rows of
+    // 8 KV heads behind 4096 keys, eight against one, both launches: 128 pairs 20.6 and 25.8
+    // us, 384 35.0 and 36.7, 512 40.8 and 40.5, 640 50.5 and 47.9, 1024 68.6 and 61.7.
     const long long pairs = (long long)a.T * a.Hkv;
     if (pairs <= 4LL * num_sms) {
         cfg.gridDim = dim3((unsigned)pairs);

@@ -35,9 +35,11 @@
 // and in P (64 rows: 357 us at first and 432 for many calls, with the rows that
 // follow in memory 384 and 460).  Above that, warps without rows skip the softmax;
 // 33 to 64 rows laid out twice gained 2% there but cost the shorter tiles 14%.
-// Measured (hd 128, 8 KV heads, 32 heads): 16 rows behind 16384 keys 45.5 us, of
-// which HBM streams 28; 64 rows with 8191 own keys behind 32768 361 us, 97% of the
-// copy rate; 6 chunks of 257 to 511 tokens behind 16384 keys 693 us, 870 TFLOP/s.
+// Measured (hd 128, 8 KV heads, 32 heads; a burst of ten calls, and call after call
+// for a second, when the power limit lowers the clock): 16 rows behind 16384 keys 46 us
+// both ways, of which HBM streams 28; 64 rows with 8191 own keys behind 32768 366 us, 95%
+// of the copy rate, and 415 to 435 (82%); 6 chunks of 257 to 511 tokens behind 16384
+// keys 694 us, 870 TFLOP/s, and 770 (781), the tensor pipe active 41% of the time.
 // Tensor memory columns: O_0 [0,128) O_1 [128,256) S_0 / P_0 [256,384)
 // S_1 / P_1 [384,512).  A stream's products complete in issue order, so S_x(next)
 // (issued after P_x V) overwrites P_x only once it was read, and its completion

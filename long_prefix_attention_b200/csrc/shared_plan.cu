@@ -6,8 +6,9 @@
 // tiles give the tile list, the cost and the partial rows before each tile.  Bound by
 // latency: some ten sums over the block, one after the other (10 us for 16 to 64
 // rows, 14 for 600, 56 for 4096); a step's layers share one plan.  A step of few
-// rows and tokens takes 128 threads, whose sums are shorter (16 rows: 10.1 us, with
-// 1024 threads 12.2), longer ones 1024.
+// rows and tokens takes 128 threads, whose sums are shorter, longer ones 1024 (in a
+// captured graph, 128 against 1024: 16 rows 8.5 and 10.7 us, 100 8.5 and 11.0, 128 11.0
+// and 11.2, 129 12.2 and 11.2, 400 20.9 and 12.7).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
