@@ -524,10 +524,10 @@ asm_status asm_decode_step_search(const void *q, const void *q_search,
  * the pages asked for by the rows up to it exceed the free ones; pages
  * returned by this step serve the next one.  A refused row keeps its length
  * and pages, its tokens keep their places in the batch and get slot -1 (what
- * the step's attention writes for them means nothing).  Lengths below 0 or above the table are
- * clamped.  The step's inputs are not changed (the ring and the table only
- * where nothing is read), so outputs may not be the inputs: feed seq_len and
- * pool_out to the next call.  No workspace; one launch.
+ * the step's attention writes for them means nothing).  Lengths below 0 or
+ * above the table are clamped.  The step's inputs are not changed (the ring and
+ * the table only where nothing is read), so outputs may not be the inputs: feed
+ * seq_len and pool_out to the next call.  No workspace; one launch.
  */
 asm_status asm_page_step(const int32_t *kv_len, const int32_t *new_len,
                          const int32_t *pos_base, int R, int page_size,
@@ -661,10 +661,13 @@ asm_status asm_shared_plan(const int32_t *q_off, const int32_t *seq_len,
  * [0, n_pages) reads as zeros and sets the error word to ASM_ERR_INVALID_ARG,
  * and so does a plan of other sizes, with which the call writes nothing; a
  * device-side wait that gives up sets ASM_ERR_TIMEOUT (outputs not valid).
- * (out, lse_out) is an attention state: with asm_decode_step over no local tokens and asm_merge_states it joins the
- * memory's retrieved state in place of an explicit prefix.
+ * (out, lse_out) is an attention state: with asm_decode_step over no local
+ * tokens and asm_merge_states it joins the memory's retrieved state in place of
+ * an explicit prefix.
  * bf16 runs on the tcgen05 tensor cores (bf16 products and weights, fp32
- * accumulators, statistics and joins), fp32 on CUDA cores.  Two launches, with
+ * accumulators, statistics and joins), fp32 on CUDA cores.  Outputs are summed
+ * before they are divided by the weights' sum: values above 2^120 over the number
+ * of keys may overflow to infinity.  Two launches, with
  * programmatic dependent launch; equal calls give equal bits.
  */
 size_t asm_shared_attention_workspace_size(int T, int Hq, int Hkv, int d);

@@ -535,7 +535,8 @@ asm_status asm_shared_attention(const void *q, const void *k_pages, const void *
     if (!aligned(ws, 16) || ws_bytes < ws_need) return ASM_ERR_WORKSPACE;
     // inputs are read while outputs and partial states are written: no output within
     // an input or another output
-    const size_t es = dt == ASM_BF16 ? 2 : 4, bytes = (size_t)T * Hq * d * es, cache = (size_t)n_pages * Hkv * page_size * d * es;
+    const size_t es = dt == ASM_BF16 ? 2 : 4, bytes = (size_t)T * Hq * d * es;
+    const size_t cache = (size_t)n_pages * Hkv * page_size * d * es;
     const void *wr[3] = {out, lse_out, ws};
     const size_t wr_n[3] = {bytes, lse_out ? 4 * (size_t)T * Hq : 0, ws_need};
     const void *rd[6] = {q, k_pages, v_pages, table, prefix_table, plan};

@@ -11,8 +11,9 @@
 // fraction of the turn whatever p is (error p 2^-64 turns; with the product in one
 // fp64 word 3.5e-8 turns at p = 2^31).  Its top 32 bits (rounded) are kept, within
 // 2^-32 turns in all; the top two of them (rounded) pick the quarter; the rest, at
-// most an eighth of a turn, loses nothing that fp32 holds.  bf16 outputs take the hardware sine and cosine there (absolute
-// error 2^-21, far below the 2^-9 of the rounding); fp32 ones sincospif.
+// most an eighth of a turn, loses nothing that fp32 holds.  bf16 outputs take the
+// hardware sine and cosine there (absolute error 2^-21, far below the 2^-9 of the
+// rounding); fp32 ones sincospif.
 //
 // Bound by memory: one read and one write of every element.  A thread keeps
 // one unit of every head (two 16-byte vectors that hold whole pairs), so the
@@ -55,7 +56,8 @@ __device__ __forceinline__ unsigned long long turns(double f) {
     double t = f * c0, e = fma(f, c0, -t) + f * c1;
     t -= rint(t);
     e -= rint(e);
-    const unsigned long long hi = t >= 0.5 ? 0x8000000000000000ull : (unsigned long long)__double2ll_rn(t * 18446744073709551616.0);
+    const unsigned long long hi = t >= 0.5 ? 0x8000000000000000ull
+                                           : (unsigned long long)__double2ll_rn(t * 18446744073709551616.0);
     return hi + (unsigned long long)__double2ll_rn(e * 18446744073709551616.0);
 }
 
