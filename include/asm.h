@@ -657,7 +657,8 @@ asm_status asm_shared_plan(const int32_t *q_off, const int32_t *seq_len,
  * row's length) never reach its result, whatever their pages hold, infinities
  * and NaN among it; an infinite value or a NaN that it does see makes its
  * column infinite or NaN, however small the key's weight (short tiles search
- * for them once more, which costs about 2 us per 128 keys).  A page id outside
+ * for them once more, which costs about 2 us per 128 keys); behind a score of
+ * -inf it may show or not.  A page id outside
  * [0, n_pages) reads as zeros and sets the error word to ASM_ERR_INVALID_ARG,
  * and so does a plan of other sizes, with which the call writes nothing; a
  * device-side wait that gives up sets ASM_ERR_TIMEOUT (outputs not valid).

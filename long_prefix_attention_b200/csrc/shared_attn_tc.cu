@@ -846,7 +846,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
                     }
                     const float mt = mraw * sl2;
                     float alpha = 1.f;
-                    if (live && !(mt <= m_used + kRescale)) {   // a NaN passes, and stays
+                    if (live && !(mt <= m_used + kRescale)) {   // a NaN passes, and stays in the sum
                         alpha = ex2f(m_used - mt);
                         m_used = mt;
                         l *= alpha;
@@ -901,7 +901,7 @@ shared_attn_tc_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
             // zero weights of rows that saw scores of -inf alone.  A vote per unit that keeps
             // such rows off the polynomial costs tall tiles 2.8%.
             if (m_used == -kNegInf) l = m_used - m_used;
-            if (m_used == kNegInf) l = 0.f;
+            if (m_used == kNegInf && l == l) l = 0.f;   // a NaN maximum gives way to a later unit's -inf, its sum stays
             if (joint) {
                 sm.ml[x][row] = make_float2(m_used, l);
                 wait(&sm.o_full[0], on[0] & 1);

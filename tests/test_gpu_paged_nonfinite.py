@@ -148,3 +148,20 @@ def test_an_infinite_value_behind_a_weight_that_underflows(dt, tok, low):
     assert same[odd][..., keep].all().item()
     keep[[3, 11, 17, 25]] = False
     assert same[..., keep].all().item()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("new,seq", [(1, 132), (6, 132), (20, 132), (40, 132), (70, 190), (100, 300)])
+def test_a_nan_key_before_units_that_a_row_does_not_see(dt, new, seq):
+    """The NaN of an early key reaches output and lse of every token, whether or not a later
+    unit of its tile holds no key that it sees."""
+    b = Batch(dt, 32, 8, 64, 32, new=[new] * 40, seq=[seq] * 40, seed=35)     # 320 lists: most are one worker's
+    clean, clse = b.run()
+    for r in range(10):
+        b.kd[int(b.table[r, 0]), 1, 3, 5] = math.nan
+    out, lse = b.run()
+    nan = torch.zeros_like(lse, dtype=torch.bool)
+    nan[:10 * new, 4:8] = True
+    assert torch.isnan(out[nan]).all().item() and torch.isnan(lse[nan]).all().item()
+    out[nan], lse[nan] = clean[nan], clse[nan]
+    assert torch.equal(out, clean) and torch.equal(lse, clse)
